@@ -427,6 +427,223 @@ SLIKL_API slikl_status slikl_grad_recompute_p(const slikl_problem *problem,
                                               size_t workspace_bytes, void *stream,
                                               const slikl_options *options);
 
+/*
+ * ---------------------------------------------------------------------------------------
+ * q and k from the projections' outputs, and the gradient back to them
+ *
+ * The indexer's q and k are the outputs x of two projections, normalised head by head and turned
+ * by the row's position. For every head of every row, over its D values:
+ *   RMS norm    r = 1 / sqrt(mean(x^2) + eps),           z = x r gain
+ *   layer norm  m = mean(x), r = 1 / sqrt(mean((x - m)^2) + eps),  z = (x - m) r gain + bias
+ *   no norm     z = x
+ * then, for the first rot_dim dims, y = z turned by the row's angles, (a, b) ->
+ * (a cos - b sin, b cos + a sin), where (a, b) are dims (i, i + rot_dim/2) (SLIKL_ROT_HALVES) or
+ * (2i, 2i + 1) (SLIKL_ROT_PAIRS), i < rot_dim/2; the other dims are y = z. Sums are fp32, and y is
+ * rounded once to the 16-bit type. (A bf16 x whose squares overflow fp32, |x| above about 1e18,
+ * is outside the norms' range.)
+ *
+ * The gradient, with dz = dy turned back and xhat = (x - m) r (m = 0 for RMS):
+ *   dgain = sum dz xhat, dbias = sum dz   (over all heads of all rows; fp32, the same bits each call)
+ *   u = dz gain,  dx = r (u - [layer: mean(u)] - xhat mean(u xhat));  no norm: dx = dz.
+ *
+ * 8-bit checkpoints. A checkpoint of x is, for each head of each row, scale = max|x| / 448 (fp32;
+ * 0 for a zero row, at least the smallest normal fp32 number otherwise) and the D values x / scale
+ * rounded to e4m3. The forward call can write one beside y in the same pass, both calls can read
+ * one in place of x, and the gradient is then the one at scale * value. A value that is not
+ * finite makes its whole row of the checkpoint NaN, scale excepted.
+ *
+ * Positions: row t stands at positions[t], or, where positions is NULL, at t % S. A row at -1 is
+ * padding: its y, checkpoint and dx are 0 and it takes no part in dgain and dbias. Any other
+ * position outside [0, table_rows) sets SLIKL_DEV_BAD_POSITION and is handled like -1.
+ * ---------------------------------------------------------------------------------------
+ */
+#define SLIKL_NORM_NONE  0
+#define SLIKL_NORM_RMS   1
+#define SLIKL_NORM_LAYER 2
+
+#define SLIKL_ROT_HALVES 0
+#define SLIKL_ROT_PAIRS  1
+
+#define SLIKL_DEV_BAD_POSITION 0x80u  /* a position was < -1 or >= table_rows                  */
+#define SLIKL_DEV_BAD_WEIGHT   0x100u /* key weights: a weight at a valid slot was not in [0, 2];
+                                         it counted as the nearest end, NaN as 0             */
+
+/* One side (queries or keys) of a call. */
+typedef struct {
+    int64_t T;              /* rows, >= 0 (T * N < 2^31); 0 = this side has none, its tensors are
+                               not looked at (dgain and dbias, where given, become 0)            */
+    int64_t S;              /* rows of a batch, >= 1, for positions = NULL; else not read         */
+    int64_t N;              /* heads of a row, 1..128                                             */
+    int64_t x_stride;       /* elements from one row of x to the next: 0 = N*D (rows dense), else
+                               a multiple of 8, >= N*D; x may be a slice of a wider projection    */
+    int64_t dx_stride;      /* the same of dx                                                     */
+    int32_t norm;           /* SLIKL_NORM_*                                                       */
+    int32_t reserved;       /* 0                                                                  */
+} slikl_qk_side;
+
+typedef struct {
+    int32_t dtype;          /* of x, y, dy, dx: SLIKL_FP16 or SLIKL_BF16                          */
+    int32_t rot_layout;     /* SLIKL_ROT_HALVES or SLIKL_ROT_PAIRS                                */
+    int64_t D;              /* head dim, 64 or 128                                                */
+    int64_t rot_dim;        /* rotated dims: a multiple of 16, 0..D (0: no rotation)              */
+    int64_t table_rows;     /* rows of cos_sin, 1 .. 2^31 - 1 (not read with rot_dim = 0)         */
+    float eps;              /* > 0, finite                                                        */
+    int32_t reserved;       /* 0                                                                  */
+    slikl_qk_side q, k;
+} slikl_qk_problem;
+
+/* Device pointers, 16-byte aligned except positions, x8_scale, keep8_scale (4 bytes). Unless a
+ * stride says otherwise tensors are dense. y may be x itself, and dx may be dy or x itself, when
+ * both have the same strides; other overlaps of outputs with anything are not allowed. */
+typedef struct {
+    const void *x;              /* dtype [T][N][D], rows x_stride apart; NULL = read x8           */
+    const void *x8;             /* e4m3  [T][N][D], a checkpoint of x; read when x is NULL        */
+    const float *x8_scale;      /* fp32  [T][N]                                                   */
+    const int32_t *positions;   /* int32 [T], or NULL: t % S                                      */
+    const float *gain;          /* fp32  [D], or NULL: ones (must be NULL without a norm)          */
+    const float *bias;          /* fp32  [D], or NULL: zeros (layer norm only)                    */
+    void *y;                    /* forward out: dtype [T][N][D]; NULL only beside keep8           */
+    void *keep8;                /* forward out: e4m3 [T][N][D], or NULL: no checkpoint (needs x)   */
+    float *keep8_scale;         /* forward out: fp32 [T][N], given exactly when keep8 is          */
+    const void *dy;             /* gradient: dtype [T][N][D]                                      */
+    void *dx;                   /* gradient out: dtype [T][N][D], rows dx_stride apart            */
+    float *dgain;               /* gradient out: fp32 [D], or NULL (must be NULL without a norm)   */
+    float *dbias;               /* gradient out: fp32 [D], or NULL (layer norm only)              */
+} slikl_qk_side_tensors;
+
+typedef struct {
+    slikl_qk_side_tensors q, k;
+    const float *cos_sin;       /* fp32 [table_rows][rot_dim]: the cosines of a position's
+                                   rot_dim/2 angles, then the sines; not read with rot_dim = 0    */
+    uint32_t *status;           /* optional device word: the call ORs SLIKL_DEV_BAD_POSITION in
+                                   (the caller clears it; slikl_read_device_status reads it)      */
+} slikl_qk_tensors;
+
+/*
+ * Forward: y (and the checkpoints asked for) of both sides in one launch. Needs no workspace.
+ * Errors: SLIKL_ERR_PARAM_NULLPTR (problem, tensors, or a tensor the sides need is NULL),
+ * SLIKL_ERR_PARAM_INVALID (values outside the sets above, misaligned pointers), SLIKL_ERR_CUDA.
+ */
+SLIKL_API slikl_status slikl_qk_norm_rope(const slikl_qk_problem *problem,
+                                          const slikl_qk_tensors *tensors, void *stream);
+
+/*
+ * Gradient, in the two-phase form (phase 1 host only): dx, dgain and dbias of both sides. The
+ * workspace (256-byte aligned) holds the partial sums of dgain and dbias.
+ * Errors: as above; SLIKL_ERR_INNER_NULLPTR, SLIKL_ERR_WORKSPACE_TOO_SMALL.
+ */
+SLIKL_API slikl_status slikl_qk_norm_rope_grad_workspace_size(const slikl_qk_problem *problem,
+                                                              size_t *workspace_bytes);
+SLIKL_API slikl_status slikl_qk_norm_rope_grad(const slikl_qk_problem *problem,
+                                               const slikl_qk_tensors *tensors, void *workspace,
+                                               size_t workspace_bytes, void *stream);
+
+/*
+ * slikl_grad_ex from the projections: forms q and k from x (or its checkpoint) in the workspace,
+ * runs slikl_grad_ex on them, and takes dq, dk back to dx, dgain and dbias. qk must describe the
+ * same rows, heads, D and dtype as problem (q: T = T1, N = N1; k: T = T2, N = 1). tensors->q, k,
+ * dq and dk, and y, keep8, dy and status of qk_tensors, are not looked at. Same streams, workspace
+ * and status-word rules as slikl_grad_ex, whose status word also receives SLIKL_DEV_BAD_POSITION.
+ * A padding row's q or k is 0 here (its position is -1), which leaves it to sparse_indices and the
+ * used lengths to keep the row out of the loss.
+ * Errors: those of the three calls.
+ */
+SLIKL_API slikl_status slikl_grad_projected_workspace_size(const slikl_problem *problem,
+                                                           const slikl_qk_problem *qk,
+                                                           const slikl_options *options,
+                                                           size_t *workspace_bytes);
+SLIKL_API slikl_status slikl_grad_projected(const slikl_problem *problem,
+                                            const slikl_qk_problem *qk,
+                                            const slikl_tensors *tensors,
+                                            const slikl_qk_tensors *qk_tensors, void *workspace,
+                                            size_t workspace_bytes, void *stream,
+                                            const slikl_options *options);
+
+/*
+ * ---------------------------------------------------------------------------------------
+ * The weight that the queries put on each key, and a cache cut to the keys that carry most of it
+ *
+ * slikl_key_weights: for every key row,
+ *   out = decay * scores + sum over the valid slots that name the key of weights,
+ * with weights the attention of the call's query rows over their slots (attn_softmax_l1norm,
+ * softmax_out, or the p of slikl_grad_recompute_p). Layouts, used lengths and valid slots are
+ * slikl_grad's; dtype, N1, D and deterministic of the problem are not read. Every key row is
+ * written (unused ones as decay * scores). With decay = 0 scores is not read.
+ *
+ * Weights are summed as 64-bit integers in units of 2^-u, u = min(40, 61 - ceil(log2(T1 * topk))),
+ * so the result has the same bits whatever the order; each weight is rounded to a multiple of
+ * 2^-u once. A valid slot's weight lies in [0, 2].
+ * ---------------------------------------------------------------------------------------
+ */
+typedef struct {
+    const int32_t *sparse_indices;  /* int32 [.., 1, topk] as in slikl_tensors                   */
+    const float *weights;           /* fp32  [.., 1, topk]; not read at invalid slots' values    */
+    const int32_t *cu_seqlens_q;    /* int32 [B+1], TND query side only, else NULL               */
+    const int32_t *cu_seqlens_k;    /* int32 [B+1], TND key side only, else NULL                 */
+    const float *scores;            /* fp32  [B,S2] / [T2], or NULL: zeros                       */
+    float *out;                     /* out fp32 [B,S2] / [T2]; may be scores itself              */
+    uint32_t *status;               /* optional device word: the call ORs SLIKL_DEV_* bits in    */
+} slikl_key_weights_tensors;
+
+/*
+ * Two-phase call; of the options only seq_used_q and seq_used_k are read (NULL = none).
+ * Errors: as slikl_grad_workspace_size / slikl_grad; SLIKL_ERR_PARAM_INVALID also for a decay that
+ * is negative or not finite.
+ */
+SLIKL_API slikl_status slikl_key_weights_workspace_size(const slikl_problem *problem,
+                                                        size_t *workspace_bytes);
+SLIKL_API slikl_status slikl_key_weights(const slikl_problem *problem,
+                                         const slikl_key_weights_tensors *tensors, float decay,
+                                         void *workspace, size_t workspace_bytes, void *stream,
+                                         const slikl_options *options);
+
+/*
+ * slikl_evict: cuts a cache of key rows to at most `budget` rows per sequence. A sequence of n
+ * rows (seq_used_k[b], else its key count) keeps all of them when n <= budget. Else it keeps its
+ * first `sinks` rows, its last `recent` rows and, of the others, the budget - sinks - recent with
+ * the highest scores (equal scores: the lower row; NaN ranks below everything). Kept rows stay in
+ * order. Row j of a sequence of the result is row kept[b][j] of the cache:
+ *   kept [B][budget]       local indices, ascending, -1 behind the last one
+ *   lengths [B]            rows kept: the seq_used_k of the result
+ *   scores_out [B][budget] their scores, 0 behind the last one
+ *   caches                 up to SLIKL_EVICT_MAX_CACHES tensors whose rows go along: in
+ *                          [B][S2][row_bytes] / [T2][row_bytes], out [B][budget][row_bytes];
+ *                          rows behind the last kept one are left as they were.
+ */
+#define SLIKL_EVICT_MAX_CACHES 8
+
+typedef struct {
+    int32_t layout_k;        /* SLIKL_BSND or SLIKL_TND */
+    int32_t n_caches;        /* 0..SLIKL_EVICT_MAX_CACHES */
+    int64_t B, S2, T2;       /* as in slikl_problem; TND: S2 = 0 or the longest sequence's rows, which
+                                only chooses how many multiprocessors share a sequence             */
+    int64_t budget;          /* rows a sequence may keep: 1 <= budget, B * budget < 2^31           */
+    int64_t sinks, recent;   /* >= 0, sinks + recent <= budget                                     */
+} slikl_evict_problem;
+
+typedef struct {
+    const void *in;          /* device, 16-byte aligned */
+    void *out;               /* device, 16-byte aligned; no overlap with any input or output */
+    int64_t row_bytes;       /* bytes of one key row, a positive multiple of 16 */
+} slikl_evict_cache;
+
+typedef struct {
+    const float *scores;            /* fp32  [B,S2] / [T2]                                       */
+    const int32_t *cu_seqlens_k;    /* int32 [B+1], TND only, else NULL                          */
+    const int32_t *seq_used_k;      /* int32 [B] rows in use, or NULL: all                       */
+    int32_t *kept;                  /* out int32 [B][budget]                                     */
+    int32_t *lengths;               /* out int32 [B]                                             */
+    float *scores_out;              /* out fp32  [B][budget], or NULL; not scores itself         */
+    uint32_t *status;               /* optional device word: the call ORs SLIKL_DEV_BAD_CU_SEQLENS_K
+                                       and SLIKL_DEV_BAD_SEQ_USED in                             */
+    slikl_evict_cache caches[SLIKL_EVICT_MAX_CACHES];
+} slikl_evict_tensors;
+
+/* Needs no workspace. Errors: SLIKL_ERR_PARAM_NULLPTR, SLIKL_ERR_PARAM_INVALID (values outside the
+ * sets above, misaligned or overlapping pointers), SLIKL_ERR_CUDA. */
+SLIKL_API slikl_status slikl_evict(const slikl_evict_problem *problem,
+                                   const slikl_evict_tensors *tensors, void *stream);
+
 /* Human-readable name of a status code (static string, never NULL). */
 SLIKL_API const char *slikl_status_string(slikl_status status);
 

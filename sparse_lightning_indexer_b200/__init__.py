@@ -10,9 +10,10 @@ sm_100 device is present the calls raise.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
-from typing import Optional
+from typing import NamedTuple, Optional, Sequence
 
 import torch
 
@@ -38,11 +39,24 @@ SLIKL_DEV_WAIT_TIMEOUT = 0x8
 SLIKL_DEV_KEY_RANGE_ABOVE_S2 = 0x10
 SLIKL_DEV_BAD_SEQ_USED = 0x20
 SLIKL_DEV_ROW_LEN_BELOW_KEYS = 0x40
+SLIKL_DEV_BAD_POSITION = 0x80
+SLIKL_DEV_BAD_WEIGHT = 0x100
 
 SLIKL_DK_AUTO = 0
 SLIKL_DK_SCATTER = 1
 SLIKL_DK_KEYMAJOR = 2
 _DK_PATHS = {"auto": SLIKL_DK_AUTO, "scatter": SLIKL_DK_SCATTER, "keymajor": SLIKL_DK_KEYMAJOR}
+
+SLIKL_NORM_NONE = 0
+SLIKL_NORM_RMS = 1
+SLIKL_NORM_LAYER = 2
+SLIKL_ROT_HALVES = 0
+SLIKL_ROT_PAIRS = 1
+_NORMS = {"none": SLIKL_NORM_NONE, "rms": SLIKL_NORM_RMS, "layer": SLIKL_NORM_LAYER}
+_ROTS = {"halves": SLIKL_ROT_HALVES, "pairs": SLIKL_ROT_PAIRS}
+_LAYOUTS = {"BSND": SLIKL_BSND, "TND": SLIKL_TND}
+
+SLIKL_EVICT_MAX_CACHES = 8
 
 EXPORTED = ("slikl_grad_workspace_size", "slikl_grad", "slikl_grad_with_events",
             "slikl_grad_workspace_size_ex", "slikl_grad_ex", "slikl_grad_dk_path",
@@ -50,7 +64,11 @@ EXPORTED = ("slikl_grad_workspace_size", "slikl_grad", "slikl_grad_with_events",
             "slikl_grad_metadata_size", "slikl_grad_metadata_workspace_size",
             "slikl_grad_metadata", "slikl_status_string", "slikl_grad_noalloc",
             "slikl_dense_grad_workspace_size", "slikl_dense_grad", "slikl_dense_grad_dk_path",
-            "slikl_grad_recompute_p_workspace_size", "slikl_grad_recompute_p")
+            "slikl_grad_recompute_p_workspace_size", "slikl_grad_recompute_p",
+            "slikl_qk_norm_rope", "slikl_qk_norm_rope_grad_workspace_size",
+            "slikl_qk_norm_rope_grad", "slikl_grad_projected_workspace_size",
+            "slikl_grad_projected", "slikl_key_weights_workspace_size", "slikl_key_weights",
+            "slikl_evict")
 
 SLIKL_NOALLOC_SCRATCH_BYTES = 32 << 20
 
@@ -94,6 +112,53 @@ class slikl_options(ctypes.Structure):
                 ("fused_end", ctypes.c_void_p), ("dk_begin", ctypes.c_void_p),
                 ("dk_end", ctypes.c_void_p), ("loss", ctypes.c_void_p),
                 ("seq_used_q", ctypes.c_void_p), ("seq_used_k", ctypes.c_void_p)]
+
+
+class slikl_qk_side(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("S", ctypes.c_int64), ("N", ctypes.c_int64),
+                ("x_stride", ctypes.c_int64), ("dx_stride", ctypes.c_int64),
+                ("norm", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class slikl_qk_problem(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("rot_layout", ctypes.c_int32), ("D", ctypes.c_int64),
+                ("rot_dim", ctypes.c_int64), ("table_rows", ctypes.c_int64),
+                ("eps", ctypes.c_float), ("reserved", ctypes.c_int32), ("q", slikl_qk_side),
+                ("k", slikl_qk_side)]
+
+
+class slikl_qk_side_tensors(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_void_p) for name in
+                ("x", "x8", "x8_scale", "positions", "gain", "bias", "y", "keep8", "keep8_scale",
+                 "dy", "dx", "dgain", "dbias")]
+
+
+class slikl_qk_tensors(ctypes.Structure):
+    _fields_ = [("q", slikl_qk_side_tensors), ("k", slikl_qk_side_tensors),
+                ("cos_sin", ctypes.c_void_p), ("status", ctypes.c_void_p)]
+
+
+class slikl_key_weights_tensors(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_void_p) for name in
+                ("sparse_indices", "weights", "cu_seqlens_q", "cu_seqlens_k", "scores", "out",
+                 "status")]
+
+
+class slikl_evict_problem(ctypes.Structure):
+    _fields_ = [("layout_k", ctypes.c_int32), ("n_caches", ctypes.c_int32), ("B", ctypes.c_int64),
+                ("S2", ctypes.c_int64), ("T2", ctypes.c_int64), ("budget", ctypes.c_int64),
+                ("sinks", ctypes.c_int64), ("recent", ctypes.c_int64)]
+
+
+class slikl_evict_cache(ctypes.Structure):
+    # the C field "in" is a keyword here
+    _fields_ = [("in_", ctypes.c_void_p), ("out", ctypes.c_void_p), ("row_bytes", ctypes.c_int64)]
+
+
+class slikl_evict_tensors(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_void_p) for name in
+                ("scores", "cu_seqlens_k", "seq_used_k", "kept", "lengths", "scores_out",
+                 "status")] + [("caches", slikl_evict_cache * SLIKL_EVICT_MAX_CACHES)]
 
 
 def make_options(dk_path="auto", fused_begin: int = 0, fused_end: int = 0, dk_begin: int = 0,
@@ -165,11 +230,30 @@ def load_library() -> ctypes.CDLL:
                                                P(slikl_tensors), VP, VP, VP, VP, ctypes.c_size_t,
                                                VP, P(slikl_options)]
         lib.slikl_grad_recompute_p.restype = ctypes.c_int32
+        lib.slikl_qk_norm_rope.argtypes = [P(slikl_qk_problem), P(slikl_qk_tensors), VP]
+        lib.slikl_qk_norm_rope_grad_workspace_size.argtypes = [P(slikl_qk_problem),
+                                                               P(ctypes.c_size_t)]
+        lib.slikl_qk_norm_rope_grad.argtypes = [P(slikl_qk_problem), P(slikl_qk_tensors), VP,
+                                                ctypes.c_size_t, VP]
+        lib.slikl_grad_projected_workspace_size.argtypes = [
+            P(slikl_problem), P(slikl_qk_problem), P(slikl_options), P(ctypes.c_size_t)]
+        lib.slikl_grad_projected.argtypes = [P(slikl_problem), P(slikl_qk_problem),
+                                             P(slikl_tensors), P(slikl_qk_tensors), VP,
+                                             ctypes.c_size_t, VP, P(slikl_options)]
+        lib.slikl_key_weights_workspace_size.argtypes = [P(slikl_problem), P(ctypes.c_size_t)]
+        lib.slikl_key_weights.argtypes = [P(slikl_problem), P(slikl_key_weights_tensors),
+                                          ctypes.c_float, VP, ctypes.c_size_t, VP,
+                                          P(slikl_options)]
+        lib.slikl_evict.argtypes = [P(slikl_evict_problem), P(slikl_evict_tensors), VP]
         lib.slikl_status_string.argtypes = [ctypes.c_int32]
         lib.slikl_status_string.restype = ctypes.c_char_p
         for name in ("slikl_grad_workspace_size", "slikl_grad", "slikl_grad_with_events",
                      "slikl_grad_workspace_size_ex", "slikl_grad_ex", "slikl_read_device_status",
-                     "slikl_grad_metadata_workspace_size", "slikl_grad_metadata"):
+                     "slikl_grad_metadata_workspace_size", "slikl_grad_metadata",
+                     "slikl_qk_norm_rope", "slikl_qk_norm_rope_grad_workspace_size",
+                     "slikl_qk_norm_rope_grad", "slikl_grad_projected_workspace_size",
+                     "slikl_grad_projected", "slikl_key_weights_workspace_size",
+                     "slikl_key_weights", "slikl_evict"):
             getattr(lib, name).restype = ctypes.c_int32
         _lib = lib
     return _lib
@@ -581,3 +665,495 @@ def dense_grad_workload(wl, device="cuda", deterministic=False, stream=None, dk_
     return dense_grad(t["q"], t["k"], t["w"], t["p"], wl.layout, wl.layout, cuq, cuk,
                       mask_mode=wl.mask_mode, deterministic=deterministic, stream=stream,
                       dk_path=dk_path, loss=loss, seq_used_q=uq, seq_used_k=uk)
+
+
+# --- q and k from the projections, and the way back --------------------------------------------
+
+def slikl_qk_norm_rope(problem: slikl_qk_problem, tensors: slikl_qk_tensors,
+                       stream: int = 0) -> None:
+    rc = load_library().slikl_qk_norm_rope(ctypes.byref(problem), ctypes.byref(tensors), stream)
+    if rc != SLIKL_OK:
+        raise SliklError(rc, "slikl_qk_norm_rope")
+
+
+def slikl_qk_norm_rope_grad_workspace_size(problem: slikl_qk_problem) -> int:
+    n = ctypes.c_size_t(0)
+    rc = load_library().slikl_qk_norm_rope_grad_workspace_size(ctypes.byref(problem),
+                                                               ctypes.byref(n))
+    if rc != SLIKL_OK:
+        raise SliklError(rc, "slikl_qk_norm_rope_grad_workspace_size")
+    return int(n.value)
+
+
+def slikl_qk_norm_rope_grad(problem: slikl_qk_problem, tensors: slikl_qk_tensors, workspace: int,
+                            workspace_bytes: int, stream: int = 0) -> None:
+    rc = load_library().slikl_qk_norm_rope_grad(ctypes.byref(problem), ctypes.byref(tensors),
+                                                workspace, workspace_bytes, stream)
+    if rc != SLIKL_OK:
+        raise SliklError(rc, "slikl_qk_norm_rope_grad")
+
+
+def slikl_grad_projected_workspace_size(problem: slikl_problem, qk: slikl_qk_problem,
+                                        options: Optional[slikl_options] = None) -> int:
+    n = ctypes.c_size_t(0)
+    rc = load_library().slikl_grad_projected_workspace_size(
+        ctypes.byref(problem), ctypes.byref(qk),
+        ctypes.byref(options) if options is not None else None, ctypes.byref(n))
+    if rc != SLIKL_OK:
+        raise SliklError(rc, "slikl_grad_projected_workspace_size")
+    return int(n.value)
+
+
+def slikl_grad_projected(problem: slikl_problem, qk: slikl_qk_problem, tensors: slikl_tensors,
+                         qk_tensors: slikl_qk_tensors, workspace: int, workspace_bytes: int,
+                         stream: int = 0, options: Optional[slikl_options] = None) -> None:
+    rc = load_library().slikl_grad_projected(
+        ctypes.byref(problem), ctypes.byref(qk), ctypes.byref(tensors), ctypes.byref(qk_tensors),
+        workspace, workspace_bytes, stream, ctypes.byref(options) if options is not None else None)
+    if rc != SLIKL_OK:
+        raise SliklError(rc, "slikl_grad_projected")
+
+
+class Checkpoint(NamedTuple):
+    """8-bit checkpoint of a 16-bit tensor [.., N, D]: scale * values, with e4m3 `values` [.., N, D]
+    (torch.float8_e4m3fn) and fp32 `scale` [.., N]; `dtype` is the type it stands for."""
+    values: torch.Tensor
+    scale: torch.Tensor
+    dtype: torch.dtype
+
+
+@contextlib.contextmanager
+def _on_stream(device: torch.device, stream):
+    with torch.cuda.device(device):
+        if stream is None:
+            yield torch.cuda.current_stream(device)
+        else:
+            with torch.cuda.stream(stream):
+                yield stream
+
+
+def _check(t, name, device, dtype, shape=None):
+    """Device address of a contiguous CUDA tensor of this device, type and shape; None for None."""
+    if t is None:
+        return None
+    if t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor on {device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _row_stride(t, name):
+    """Elements from one row to the next of t [B, S, N, D] or [T, N, D] whose heads are dense."""
+    shape, st = t.shape, t.stride()
+    N, D = shape[-2], shape[-1]
+    dense = N * D
+    if t.numel() == 0:
+        return dense
+    row = dense
+    if st[-1] != 1 or (N > 1 and st[-2] != D):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
+    if t.dim() == 3:
+        if shape[0] > 1:
+            row = st[0]
+    elif shape[1] > 1:
+        row = st[1]
+        if shape[0] > 1 and st[0] != shape[1] * row:
+            raise ValueError(f"{name}: the batches must follow one another at the rows' stride")
+    elif shape[0] > 1:
+        row = st[0]
+    if row < dense or row % 8:
+        raise ValueError(f"{name}: row stride {row} is not a multiple of 8 of at least N*D = {dense}")
+    return row
+
+
+def _qk_side(x, name, layout, device, positions, gain, bias, norm, rot):
+    """(side struct, tensor struct with what both directions read, shape, dtype) of x or its
+    Checkpoint; x None = no such side."""
+    if norm not in _NORMS:
+        raise ValueError(f"norm_{name} must be one of {sorted(_NORMS)}")
+    kind = _NORMS[norm]
+    side, tn = slikl_qk_side(0, 1, 1, 0, 0, kind, 0), slikl_qk_side_tensors()
+    if x is None:
+        return side, tn, None, None
+    src = x.values if isinstance(x, Checkpoint) else x
+    shape, D = src.shape, src.shape[-1]
+    if src.device != device or len(shape) != (4 if layout == "BSND" else 3):
+        raise ValueError(f"x_{name}: {layout} rows on {device} are wanted")
+    if isinstance(x, Checkpoint):
+        dtype = x.dtype
+        tn.x8 = _check(x.values, f"x_{name}.values", device, torch.float8_e4m3fn)
+        tn.x8_scale = _check(x.scale, f"x_{name}.scale", device, torch.float32, shape[:-1])
+    else:
+        dtype = x.dtype
+        side.x_stride = _row_stride(x, f"x_{name}")
+        tn.x = x.data_ptr()
+    side.N = shape[-2]
+    side.T = shape[0] * shape[1] if layout == "BSND" else shape[0]
+    if layout == "BSND":
+        side.S = max(1, shape[1])
+    elif positions is None and rot and side.T:
+        raise ValueError(f"TND needs pos_{name}")
+    tn.positions = _check(positions, f"pos_{name}", device, torch.int32)
+    if positions is not None and positions.numel() != side.T:
+        raise ValueError(f"pos_{name} must have {side.T} entries")
+    tn.gain = _check(gain, f"gain_{name}", device, torch.float32, (D,))
+    tn.bias = _check(bias, f"bias_{name}", device, torch.float32, (D,))
+    return side, tn, shape, dtype
+
+
+def _qk_call(x_q, x_k, cos_sin, pos, gain, bias, norm, rot_layout, eps, layouts, status):
+    """(problem, tensors, [(shape, dtype) of q, k], device) of either direction."""
+    some = x_q if x_q is not None else x_k
+    if some is None:
+        raise ValueError("x_q and x_k are both None")
+    device = (some.values if isinstance(some, Checkpoint) else some).device
+    if device.type != "cuda":
+        raise ValueError("tensors must be CUDA tensors")
+    if rot_layout not in _ROTS:
+        raise ValueError(f"rot_layout must be one of {sorted(_ROTS)}")
+    rot = 0 if cos_sin is None else cos_sin.shape[-1]
+    pr, tn, said = slikl_qk_problem(), slikl_qk_tensors(), []
+    for i, (name, x) in enumerate((("q", x_q), ("k", x_k))):
+        if layouts[i] not in _LAYOUTS:
+            raise ValueError(f"layout_{name} must be one of {sorted(_LAYOUTS)}")
+        side, t, shape, dtype = _qk_side(x, name, layouts[i], device, pos[i], gain[i], bias[i],
+                                         norm[i], rot)
+        setattr(pr, name, side)
+        setattr(tn, name, t)
+        said.append((shape, dtype))
+    (sq, dq), (sk, dk) = said
+    dtype, D = (dq, sq[-1]) if sq is not None else (dk, sk[-1])
+    if dtype not in _DT or (sq is not None and sk is not None and (dk != dtype or sk[-1] != D)):
+        raise ValueError("q and k must share D and one dtype, float16 or bfloat16")
+    pr.dtype, pr.rot_layout, pr.D, pr.rot_dim, pr.eps = _DT[dtype], _ROTS[rot_layout], D, rot, eps
+    if cos_sin is not None:
+        if cos_sin.dim() != 2:
+            raise ValueError("cos_sin must be [positions, rotated dims]")
+        pr.table_rows = cos_sin.shape[0]
+        tn.cos_sin = _check(cos_sin, "cos_sin", device, torch.float32)
+    tn.status = _check(status, "status", device, torch.int32, (1,))
+    return pr, tn, said, device
+
+
+def qk_norm_rope(x_q, x_k, cos_sin=None, *, pos_q=None, pos_k=None, gain_q=None, gain_k=None,
+                 bias_q=None, bias_k=None, norm_q="rms", norm_k="rms", rot_layout="halves",
+                 eps=1e-6, layout_q="BSND", layout_k="BSND", checkpoint=False, out=None,
+                 status=None, stream=None):
+    """q and k of the indexer from the outputs of their projections (slikl_qk_norm_rope).
+
+    x_q [B,S1,N1,D] / [T1,N1,D], x_k [B,S2,N2,D] / [T2,N2,D] in float16 or bfloat16, or a
+    Checkpoint of them; either may be None. Rows may lie apart (slices of one projection's
+    output). `norm_*` is "none", "rms" or "layer" over each head, with fp32 `gain` / `bias` [D];
+    `cos_sin` fp32 [positions, R] holds the cosines of a position's R/2 angles, then the sines (None:
+    no rotation); `rot_layout` "halves" turns dims (i, i + R/2), "pairs" (2i, 2i + 1). `pos_*` are
+    int32 positions per row (-1: padding row, all zero); without them a BSND row stands at its place
+    in its batch. `status` (int32 [1]) receives SLIKL_DEV_BAD_POSITION.
+    Returns dict(q, k) and, with checkpoint=True, checkpoint_q / checkpoint_k; `out` may supply q, k.
+    """
+    pr, tn, said, device = _qk_call(x_q, x_k, cos_sin, (pos_q, pos_k), (gain_q, gain_k),
+                                    (bias_q, bias_k), (norm_q, norm_k), rot_layout, eps,
+                                    (layout_q, layout_k), status)
+    res = {}
+    with _on_stream(device, stream) as s:
+        for name, (shape, dtype), t in (("q", said[0], tn.q), ("k", said[1], tn.k)):
+            y = out.get(name) if out else None
+            if y is None and shape is not None:
+                y = torch.empty(shape, dtype=dtype, device=device)
+            res[name] = y
+            if shape is None:
+                continue
+            t.y = _check(y, name, device, dtype, shape)
+            if checkpoint:
+                c = Checkpoint(torch.empty(shape, dtype=torch.float8_e4m3fn, device=device),
+                               torch.empty(shape[:-1], dtype=torch.float32, device=device), dtype)
+                t.keep8, t.keep8_scale = c.values.data_ptr(), c.scale.data_ptr()
+                res["checkpoint_" + name] = c
+        slikl_qk_norm_rope(pr, tn, s.cuda_stream)
+    return res
+
+
+def qk_norm_rope_grad(dq, dk, x_q, x_k, cos_sin=None, *, pos_q=None, pos_k=None, gain_q=None,
+                      gain_k=None, norm_q="rms", norm_k="rms", rot_layout="halves", eps=1e-6,
+                      layout_q="BSND", layout_k="BSND", out=None, workspace=None, status=None,
+                      stream=None):
+    """The gradient of qk_norm_rope at x (or its Checkpoint): dq, dk as grad() returns them back to
+    the projections. Returns dict(dx_q, dx_k, dgain_q, dgain_k, dbias_q, dbias_k, workspace); a
+    side without a norm has no dgain, one without a layer norm no dbias. `out` may supply
+    dx_q / dx_k, whose rows may lie apart (slices of one projection's gradient)."""
+    pr, tn, said, device = _qk_call(x_q, x_k, cos_sin, (pos_q, pos_k), (gain_q, gain_k),
+                                    (None, None), (norm_q, norm_k), rot_layout, eps,
+                                    (layout_q, layout_k), status)
+    with _on_stream(device, stream) as s:
+        res = _qk_gradients(pr, tn, said, device, out)
+        for name, dy, (shape, dtype), t in (("dq", dq, said[0], tn.q), ("dk", dk, said[1], tn.k)):
+            if shape is not None:
+                if dy is None:
+                    raise ValueError(f"{name} is missing")
+                t.dy = _check(dy, name, device, dtype, shape)
+        nbytes = slikl_qk_norm_rope_grad_workspace_size(pr)
+        if workspace is None or workspace.numel() < nbytes:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        slikl_qk_norm_rope_grad(pr, tn, workspace.data_ptr(), workspace.numel(), s.cuda_stream)
+    res["workspace"] = workspace
+    return res
+
+
+def _qk_gradients(pr, tn, said, device, out):
+    """Allocates (or takes from `out`) dx, dgain and dbias and enters them in the structs."""
+    res = {}
+    for name, (shape, dtype), side, t in (("q", said[0], pr.q, tn.q), ("k", said[1], pr.k, tn.k)):
+        dx = out.get("dx_" + name) if out else None
+        res["dx_" + name] = res["dgain_" + name] = res["dbias_" + name] = None
+        if shape is None:
+            continue
+        if dx is None:
+            dx = torch.empty(shape, dtype=dtype, device=device)
+        elif dx.device != device or dx.dtype != dtype or dx.shape != shape:
+            raise ValueError(f"dx_{name} must be {dtype} {tuple(shape)} on {device}")
+        side.dx_stride = _row_stride(dx, f"dx_{name}")
+        t.dx = dx.data_ptr()
+        res["dx_" + name] = dx
+        for what, least in (("dgain", SLIKL_NORM_RMS), ("dbias", SLIKL_NORM_LAYER)):
+            if side.norm >= least:
+                g = torch.empty(shape[-1], dtype=torch.float32, device=device)
+                setattr(t, what, g.data_ptr())
+                res[f"{what}_{name}"] = g
+    return res
+
+
+def checkpoint_pack(x, stream=None) -> Checkpoint:
+    """8-bit checkpoint of x [.., N, D] (float16 or bfloat16, rows contiguous, D 64 or 128): one
+    e4m3 value an element and one fp32 scale, max|x| / 448, for each of the D-long rows."""
+    D = x.shape[-1]
+    if x.device.type != "cuda" or not x.is_contiguous() or x.dtype not in _DT:
+        raise ValueError("x must be a contiguous CUDA tensor of float16 or bfloat16")
+    rows = x.numel() // D if D else 0
+    pr, tn = _rows_problem(rows, D, x.dtype)
+    with _on_stream(x.device, stream) as s:
+        c = Checkpoint(torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device),
+                       torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device), x.dtype)
+        tn.q.x, tn.q.keep8, tn.q.keep8_scale = x.data_ptr(), c.values.data_ptr(), c.scale.data_ptr()
+        slikl_qk_norm_rope(pr, tn, s.cuda_stream)
+    return c
+
+
+def checkpoint_unpack(c: Checkpoint, stream=None) -> torch.Tensor:
+    """The tensor that a checkpoint stands for, scale * values rounded to its 16-bit type."""
+    v, D = c.values, c.values.shape[-1]
+    if v.device.type != "cuda":
+        raise ValueError("tensors must be CUDA tensors")
+    pr, tn = _rows_problem(v.numel() // D if D else 0, D, c.dtype)
+    tn.q.x8 = _check(v, "values", v.device, torch.float8_e4m3fn)
+    tn.q.x8_scale = _check(c.scale, "scale", v.device, torch.float32, v.shape[:-1])
+    with _on_stream(v.device, stream) as s:
+        x = torch.empty(v.shape, dtype=c.dtype, device=v.device)
+        tn.q.y = x.data_ptr()
+        slikl_qk_norm_rope(pr, tn, s.cuda_stream)
+    return x
+
+
+def _rows_problem(rows, D, dtype):
+    """A problem of D-long rows as they are: neither norm nor rotation."""
+    if dtype not in _DT:
+        raise ValueError("float16 or bfloat16 is wanted")
+    none = slikl_qk_side(0, 1, 1, 0, 0, SLIKL_NORM_NONE, 0)
+    return (slikl_qk_problem(_DT[dtype], SLIKL_ROT_HALVES, D, 0, 0, 1.0, 0,
+                             slikl_qk_side(rows, 1, 1, 0, 0, SLIKL_NORM_NONE, 0), none),
+            slikl_qk_tensors())
+
+
+def grad_projected(x_q, x_k, w, attn_softmax_l1norm, sparse_indices, cos_sin=None, *, pos_q=None,
+                   pos_k=None, gain_q=None, gain_k=None, bias_q=None, bias_k=None, norm_q="rms",
+                   norm_k="rms", rot_layout="halves", eps=1e-6, layout_q="BSND", layout_k="BSND",
+                   cu_seqlens_q=None, cu_seqlens_k=None, deterministic=False, stream=None, out=None,
+                   workspace=None, dk_path="auto", key_range_bound=0, loss=False, seq_used_q=None,
+                   seq_used_k=None):
+    """grad() from the outputs of the projections, or from their checkpoints: q and k as
+    qk_norm_rope forms them, the indexer's gradient, and dq, dk back as qk_norm_rope_grad takes
+    them, in one call (slikl_grad_projected). Returns dict(dx_q, dx_k, dgain_*, dbias_*, dw,
+    softmax_out, workspace[, loss]); `out` may supply dx_q / dx_k."""
+    qk, qt, said, device = _qk_call(x_q, x_k, cos_sin, (pos_q, pos_k), (gain_q, gain_k),
+                                    (bias_q, bias_k), (norm_q, norm_k), rot_layout, eps,
+                                    (layout_q, layout_k), None)
+    if x_q is None or x_k is None:
+        raise ValueError("x_q and x_k are both needed")
+    (sq, dtype), (sk, _) = said
+    pr = slikl_problem(_DT[dtype], _LAYOUTS[layout_q], _LAYOUTS[layout_k],
+                       1 if deterministic else 0)
+    pr.T1, pr.T2, pr.N1, pr.D, pr.topk = qk.q.T, qk.k.T, sq[-2], sq[-1], sparse_indices.shape[-1]
+    pr.B = _batches(layout_q, layout_k, sq[0], sk[0], cu_seqlens_q, cu_seqlens_k)
+    if layout_q == "BSND":
+        pr.S1 = sq[1]
+    pr.S2 = sk[1] if layout_k == "BSND" else int(key_range_bound)
+    i32, f32 = torch.int32, torch.float32
+    slots = tuple(sq[:-2]) + (1, pr.topk)
+    with _on_stream(device, stream) as s:
+        res = _qk_gradients(qk, qt, said, device, out)
+        res["dw"] = torch.empty(sq[:-1], dtype=f32, device=device)
+        res["softmax_out"] = torch.empty(slots, dtype=f32, device=device)
+        loss_t = torch.empty(pr.T1, dtype=f32, device=device) if loss else None
+        opt = slikl_options(_DK_PATHS[dk_path], None, None, None, None,
+                            loss_t.data_ptr() if loss else None,
+                            _check(seq_used_q, "seq_used_q", device, i32, (pr.B,)),
+                            _check(seq_used_k, "seq_used_k", device, i32, (pr.B,)))
+        tn = slikl_tensors(
+            None, None, _check(w, "w", device, f32, sq[:-1]),
+            _check(attn_softmax_l1norm, "attn_softmax_l1norm", device, f32, slots),
+            _check(sparse_indices, "sparse_indices", device, i32, slots),
+            _check(cu_seqlens_q, "cu_seqlens_q", device, i32) if layout_q == "TND" else None,
+            _check(cu_seqlens_k, "cu_seqlens_k", device, i32) if layout_k == "TND" else None,
+            None, None, res["dw"].data_ptr(), res["softmax_out"].data_ptr())
+        nbytes = slikl_grad_projected_workspace_size(pr, qk, opt)
+        if workspace is None or workspace.numel() < nbytes:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        slikl_grad_projected(pr, qk, tn, qt, workspace.data_ptr(), workspace.numel(),
+                             s.cuda_stream, opt)
+    res["workspace"] = workspace
+    if loss:
+        res["loss"] = loss_t
+    return res
+
+
+def _batches(layout_q, layout_k, rows_q, rows_k, cu_q, cu_k):
+    """The number of batches, on which both sides have to agree."""
+    said = [cu.numel() - 1 if layout == "TND" and cu is not None else rows if layout == "BSND" else -1
+            for layout, rows, cu in ((layout_q, rows_q, cu_q), (layout_k, rows_k, cu_k))]
+    if said[0] != said[1] or said[0] < 0:
+        raise ValueError("queries and keys must have the same number of batches (TND: cu_seqlens)")
+    return said[0]
+
+
+# --- weights on the keys, and a cache cut to them -----------------------------------------------
+
+def slikl_key_weights_workspace_size(problem: slikl_problem) -> int:
+    n = ctypes.c_size_t(0)
+    rc = load_library().slikl_key_weights_workspace_size(ctypes.byref(problem), ctypes.byref(n))
+    if rc != SLIKL_OK:
+        raise SliklError(rc, "slikl_key_weights_workspace_size")
+    return int(n.value)
+
+
+def slikl_key_weights(problem: slikl_problem, tensors: slikl_key_weights_tensors, decay: float,
+                      workspace: int, workspace_bytes: int, stream: int = 0,
+                      options: Optional[slikl_options] = None) -> None:
+    rc = load_library().slikl_key_weights(
+        ctypes.byref(problem), ctypes.byref(tensors), decay, workspace, workspace_bytes, stream,
+        ctypes.byref(options) if options is not None else None)
+    if rc != SLIKL_OK:
+        raise SliklError(rc, "slikl_key_weights")
+
+
+def slikl_evict(problem: slikl_evict_problem, tensors: slikl_evict_tensors,
+                stream: int = 0) -> None:
+    rc = load_library().slikl_evict(ctypes.byref(problem), ctypes.byref(tensors), stream)
+    if rc != SLIKL_OK:
+        raise SliklError(rc, "slikl_evict")
+
+
+def key_weights(weights, sparse_indices, scores, decay=1.0, layout_q="BSND", layout_k="BSND",
+                cu_seqlens_q=None, cu_seqlens_k=None, seq_used_q=None, seq_used_k=None,
+                key_range_bound=0, out=None, workspace=None, status=None, stream=None):
+    """decay * scores plus, for every key row, the weights of the slots that name it
+    (slikl_key_weights): fp32 `weights` and int32 `sparse_indices` [B,S1,1,topk] / [T1,1,topk] (p of
+    grad(), softmax_out, or p of grad_recompute_p), fp32 `scores` [B,S2] / [T2]. `out` may be
+    `scores`. `status` (int32 [1]) receives the device flags. Returns dict(scores, workspace)."""
+    device, i32, f32 = scores.device, torch.int32, torch.float32
+    if device.type != "cuda" or layout_q not in _LAYOUTS or layout_k not in _LAYOUTS:
+        raise ValueError("CUDA tensors and layouts BSND or TND are wanted")
+    shape = sparse_indices.shape
+    if len(shape) != (4 if layout_q == "BSND" else 3) or shape[-2] != 1 or \
+            scores.dim() != (2 if layout_k == "BSND" else 1):
+        raise ValueError("sparse_indices must be [B,S1,1,topk] / [T1,1,topk], scores [B,S2] / [T2]")
+    pr = slikl_problem(SLIKL_BF16, _LAYOUTS[layout_q], _LAYOUTS[layout_k], 0, 0, 0, 0, 0, 0, 1, 64,
+                       shape[-1])
+    pr.B = _batches(layout_q, layout_k, shape[0], scores.shape[0], cu_seqlens_q, cu_seqlens_k)
+    if layout_q == "BSND":
+        pr.S1 = shape[1]
+    else:
+        pr.T1 = shape[0]
+    if layout_k == "BSND":
+        pr.S2 = scores.shape[1]
+    else:
+        pr.T2, pr.S2 = scores.shape[0], int(key_range_bound)
+    opt = None
+    if seq_used_q is not None or seq_used_k is not None:
+        opt = slikl_options(0, None, None, None, None, None,
+                            _check(seq_used_q, "seq_used_q", device, i32, (pr.B,)),
+                            _check(seq_used_k, "seq_used_k", device, i32, (pr.B,)))
+    with _on_stream(device, stream) as s:
+        if out is None:
+            out = torch.empty_like(scores)
+        tn = slikl_key_weights_tensors(
+            _check(sparse_indices, "sparse_indices", device, i32),
+            _check(weights, "weights", device, f32, shape),
+            _check(cu_seqlens_q, "cu_seqlens_q", device, i32) if layout_q == "TND" else None,
+            _check(cu_seqlens_k, "cu_seqlens_k", device, i32) if layout_k == "TND" else None,
+            _check(scores, "scores", device, f32), _check(out, "out", device, f32, scores.shape),
+            _check(status, "status", device, i32, (1,)))
+        nbytes = slikl_key_weights_workspace_size(pr)
+        if workspace is None or workspace.numel() < nbytes:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        slikl_key_weights(pr, tn, decay, workspace.data_ptr(), workspace.numel(), s.cuda_stream, opt)
+    return dict(scores=out, workspace=workspace)
+
+
+def evict(scores, caches: Sequence[torch.Tensor], budget, sinks=0, recent=0, layout_k="BSND",
+          cu_seqlens_k=None, seq_used_k=None, key_range_bound=0, out=None, status=None,
+          stream=None):
+    """Cuts a cache to at most `budget` key rows a sequence (slikl_evict): the first `sinks`, the
+    last `recent` and those with the highest fp32 `scores` [B,S2] / [T2]. `caches` are up to eight
+    tensors [B,S2,..] / [T2,..] of any type whose rows (a multiple of 16 bytes) go along.
+    Returns dict(kept, lengths, scores, caches): local indices [B,budget] (-1 behind the last),
+    rows kept [B] (the seq_used_k of the result), their scores, and the caches [B,budget,..].
+    `out` may supply any of the four; rows of its caches behind the last kept one are left as they
+    were (without it they are zero)."""
+    device, i32, f32 = scores.device, torch.int32, torch.float32
+    if device.type != "cuda" or layout_k not in _LAYOUTS:
+        raise ValueError("CUDA tensors and layout BSND or TND are wanted")
+    bsnd = layout_k == "BSND"
+    if scores.dim() != (2 if bsnd else 1) or (not bsnd and cu_seqlens_k is None):
+        raise ValueError("scores must be [B,S2], or [T2] with cu_seqlens_k")
+    if len(caches) > SLIKL_EVICT_MAX_CACHES:
+        raise ValueError(f"at most {SLIKL_EVICT_MAX_CACHES} caches")
+    budget, lead = int(budget), scores.dim()
+    B = scores.shape[0] if bsnd else cu_seqlens_k.numel() - 1
+    pr = slikl_evict_problem(_LAYOUTS[layout_k], len(caches), B,
+                             scores.shape[1] if bsnd else int(key_range_bound),
+                             0 if bsnd else scores.shape[0], budget, int(sinks), int(recent))
+    if budget < 1:
+        raise ValueError("budget must be at least 1")
+    out = out or {}
+    with _on_stream(device, stream) as s:
+        kept, lengths, new = out.get("kept"), out.get("lengths"), out.get("scores")
+        if kept is None:
+            kept = torch.empty(B, budget, dtype=i32, device=device)
+        if lengths is None:
+            lengths = torch.empty(B, dtype=i32, device=device)
+        if new is None:
+            new = torch.empty(B, budget, dtype=f32, device=device)
+        outs = out.get("caches")
+        if outs is None:
+            outs = [torch.zeros(B, budget, *c.shape[lead:], dtype=c.dtype, device=device)
+                    for c in caches]
+        if len(outs) != len(caches):
+            raise ValueError("out['caches'] must have a tensor for each cache")
+        tn = slikl_evict_tensors(
+            _check(scores, "scores", device, f32),
+            None if bsnd else _check(cu_seqlens_k, "cu_seqlens_k", device, i32),
+            _check(seq_used_k, "seq_used_k", device, i32, (B,)),
+            _check(kept, "kept", device, i32, (B, budget)),
+            _check(lengths, "lengths", device, i32, (B,)),
+            _check(new, "scores (out)", device, f32, (B, budget)),
+            _check(status, "status", device, i32, (1,)))
+        for i, (c, o) in enumerate(zip(caches, outs)):
+            rest = c.shape[lead:]
+            if c.shape[:lead] != scores.shape:
+                raise ValueError(f"cache {i} must have scores' rows")
+            tn.caches[i] = (_check(c, f"cache {i}", device, c.dtype),
+                            _check(o, f"out cache {i}", device, c.dtype, (B, budget, *rest)),
+                            rest.numel() * c.element_size())
+        slikl_evict(pr, tn, s.cuda_stream)
+    return dict(kept=kept, lengths=lengths, scores=new, caches=list(outs))

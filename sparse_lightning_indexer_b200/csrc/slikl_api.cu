@@ -344,6 +344,21 @@ slikl_status slikl_grad_recompute_p(const slikl_problem *problem, const slikl_ma
 }  // extern "C"
 
 namespace slikl {
+
+slikl_status check_index_call(const slikl_problem *problem, const slikl_tensors *tensors,
+                              const slikl_options *options, bool need_all) {
+    Derived dv;
+    slikl_status st = validate(problem, &dv);
+    if (st != SLIKL_OK) return st;
+    st = check_tensors(problem, tensors, need_all);
+    if (st != SLIKL_OK) return st;
+    if (options && ((reinterpret_cast<uintptr_t>(options->loss) & 3) ||
+                    (reinterpret_cast<uintptr_t>(options->seq_used_q) & 3) ||
+                    (reinterpret_cast<uintptr_t>(options->seq_used_k) & 3)))
+        return SLIKL_ERR_PARAM_INVALID;
+    return SLIKL_OK;
+}
+
 namespace {
 
 slikl_status run_grad(const slikl_problem *problem, const slikl_tensors *tensors,
@@ -354,12 +369,8 @@ slikl_status run_grad(const slikl_problem *problem, const slikl_tensors *tensors
     if (st != SLIKL_OK) return st;
     st = choose_dk_path(problem, &dv, options ? options->dk_path : SLIKL_DK_AUTO);
     if (st != SLIKL_OK) return st;
-    st = check_tensors(problem, tensors, true);
+    st = check_index_call(problem, tensors, options, true);
     if (st != SLIKL_OK) return st;
-    if (options && ((reinterpret_cast<uintptr_t>(options->loss) & 3) ||
-                    (reinterpret_cast<uintptr_t>(options->seq_used_q) & 3) ||
-                    (reinterpret_cast<uintptr_t>(options->seq_used_k) & 3)))
-        return SLIKL_ERR_PARAM_INVALID;
     if (!workspace) return SLIKL_ERR_PARAM_NULLPTR;
     if (reinterpret_cast<uintptr_t>(workspace) & 255) return SLIKL_ERR_PARAM_INVALID;
     WsLayout L = make_layout(dv.T1, dv.T2, problem->topk, problem->D, problem->deterministic,

@@ -171,6 +171,11 @@ __device__ __forceinline__ int32_t slot_row(int32_t v, int32_t kbase, int32_t kl
     return v >= 0 && v < klen ? kbase + v : -1;
 }
 
+// The checks of a call's problem, tensors and options that slikl_grad_ex makes before its first
+// launch (need_all = false: only the indices and cu_seqlens have to be there).
+slikl_status check_index_call(const slikl_problem *problem, const slikl_tensors *tensors,
+                              const slikl_options *options, bool need_all);
+
 // kernels (defined in the .cu files)
 cudaError_t launch_metadata(const Params &P, int workers, int mode, cudaStream_t s);
 cudaError_t launch_fused_sm100(const Params &P, int workers, cudaStream_t s);

@@ -1,0 +1,382 @@
+"""GPU tests of the weights on the keys and of the cache cut to the keys that carry most of it,
+against plain fp64 forms (operators_reference.py): weights within their derived bound, kept rows and
+copied caches exactly."""
+
+import math
+
+import pytest
+import torch
+
+import slikl_inputs as si
+import sparse_lightning_indexer_b200 as sli
+import operators_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+
+def dev(t):
+    return None if t is None else t.cuda()
+
+
+def ranges(lens):
+    at, out = 0, []
+    for n in lens:
+        out.append((at, n))
+        at += n
+    return out
+
+
+def cu(lens):
+    return torch.tensor([0] + [a + n for a, n in ranges(lens)], dtype=torch.int32)
+
+
+def draw_rows(seed, lens_q, lens_k, K, invalid=0.3, dup=True):
+    """Indices (any order, repeats, -1 in between) and weights normalised over the valid slots."""
+    g = torch.Generator().manual_seed(seed)
+    idx, w = [], []
+    for qn, kn in zip(lens_q, lens_k):
+        i = torch.randint(0, max(kn, 1), (qn, K), generator=g)
+        if not dup and kn >= K and qn:
+            i = torch.stack([torch.randperm(kn, generator=g)[:K] for _ in range(qn)])
+        bad = torch.rand(qn, K, generator=g) < invalid
+        i[bad | torch.tensor(kn == 0)] = -1
+        idx.append(i)
+        w.append(torch.exp(torch.randn(qn, K, generator=g)))
+    idx, w = torch.cat(idx).to(torch.int32), torch.cat(w)
+    valid = idx >= 0
+    w = w / (w * valid).sum(-1, keepdim=True).clamp_min(1e-3)
+    w = w.clamp_max(2.0)
+    w[~valid] = float("nan")                    # never looked at
+    return idx, w
+
+
+def weights_bound(want, named, slots, scores):
+    """Half an fp32 step of the result, and half a unit 2^-u for each slot that names the key."""
+    u = min(40, 61 - math.ceil(math.log2(max(slots, 1))))
+    return want.abs() * 2.0 ** -24 + named * 2.0 ** -(u + 1) + 2.0 ** -149
+
+
+def check_weights(got, idx, w, br, bk, scores, decay, used_q=None, used_k=None):
+    want = ref.key_weights(w, idx, br, bk, scores, decay, used_q, used_k)
+    named = ref.key_weights(torch.ones_like(w), idx, br, bk, torch.zeros_like(scores), 0.0, used_q, used_k)
+    got = got.cpu().double().reshape(-1)
+    over = (got - want).abs() > weights_bound(want, named, idx.numel(), scores)
+    assert torch.isfinite(got).all() and not over.any(), (got - want).abs().max()
+
+
+# (layout, query lengths, key lengths, topk): single rows, a batch without queries, one without
+# keys, ranges on both sides of what one multiprocessor holds, rows shorter than a warp
+CASES = [
+    ("BSND", [1] * 5, [700] * 5, 33),
+    ("BSND", [40, 40], [300, 300], 200),
+    ("BSND", [1], [1], 1),
+    ("BSND", [513], [4096], 257),
+    ("BSND", [3] * 300, [50] * 300, 16),
+    ("TND", [0, 5, 3, 17], [4, 0, 6, 999], 8),
+    ("TND", [130, 1, 64], [5000, 40000, 1], 100),
+    ("TND", [600], [131072], 64),
+    ("BSND", [4] * 2, [70000] * 2, 2048),
+    ("BSND", [2000], [64], 8192),
+]
+
+
+@pytest.mark.parametrize("case", CASES, ids=lambda c: f"{c[0]}-{len(c[1])}x{max(c[1])}-{max(c[2])}-{c[3]}")
+@pytest.mark.parametrize("decay", [1.0, 0.0, 0.875])
+def test_key_weights(case, decay):
+    layout, lq, lk, K = case
+    idx, w = draw_rows(5, lq, lk, K)
+    g = torch.Generator().manual_seed(6)
+    scores = torch.rand(sum(lk), generator=g) * 10
+    B = len(lq)
+    bsnd = layout == "BSND"
+    s = scores.clone()
+    if decay == 0.0:
+        s[:] = float("nan")                     # not read
+    args = (dev(w).reshape(B, lq[0], 1, K) if bsnd else dev(w)[:, None],
+            dev(idx).reshape(B, lq[0], 1, K) if bsnd else dev(idx)[:, None],
+            dev(s).reshape(B, lk[0]) if bsnd else dev(s))
+    kw = dict(decay=decay, layout_q=layout, layout_k=layout, cu_seqlens_q=None if bsnd else dev(cu(lq)),
+              cu_seqlens_k=None if bsnd else dev(cu(lk)), key_range_bound=max(lk))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    r = sli.key_weights(*args, status=status, **kw)
+    check_weights(r["scores"], idx, w, ranges(lq), ranges(lk), scores, decay)
+    assert int(status) == 0
+    for _ in range(3):
+        assert torch.equal(sli.key_weights(*args, **kw)["scores"], r["scores"])
+    if not bsnd:                                # no promise about the longest range
+        kw["key_range_bound"] = 0
+        assert torch.equal(sli.key_weights(*args, **kw)["scores"], r["scores"])
+    own = args[2]
+    sli.key_weights(args[0], args[1], own, out=own, **kw)
+    assert torch.equal(own, r["scores"])        # in place
+
+
+@pytest.mark.parametrize("layout_q,layout_k", [("BSND", "TND"), ("TND", "BSND")])
+def test_key_weights_mixed_layouts(layout_q, layout_k):
+    lq, lk, K = [6, 6, 6], [90, 90, 90], 40
+    idx, w = draw_rows(15, lq, lk, K)
+    scores = torch.rand(sum(lk), generator=torch.Generator().manual_seed(1))
+    r = sli.key_weights(dev(w).reshape((3, 6, 1, K) if layout_q == "BSND" else (18, 1, K)),
+                        dev(idx).reshape((3, 6, 1, K) if layout_q == "BSND" else (18, 1, K)),
+                        dev(scores).reshape((3, 90) if layout_k == "BSND" else (270,)),
+                        layout_q=layout_q, layout_k=layout_k, cu_seqlens_q=dev(cu(lq)),
+                        cu_seqlens_k=dev(cu(lk)))
+    check_weights(r["scores"], idx, w, ranges(lq), ranges(lk), scores, 1.0)
+
+
+def test_key_weights_used_lengths():
+    lq, lk, K = [50] * 4, [400] * 4, 60
+    idx, w = draw_rows(7, lq, lk, K, invalid=0.1)
+    idx2 = idx.view(4, 50, K).clone()
+    used_q, used_k = [50, 0, 17, 1], [400, 300, 0, 3]
+    for b, u in enumerate(used_q):
+        idx2[b, u:] = 1 << 30                   # padding rows are not read
+    scores = torch.zeros(1600)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    i32 = dict(dtype=torch.int32, device="cuda")
+    r = sli.key_weights(dev(w).reshape(4, 50, 1, K), dev(idx2).reshape(4, 50, 1, K), dev(scores).reshape(4, 400),
+                        seq_used_q=torch.tensor(used_q, **i32), seq_used_k=torch.tensor(used_k, **i32), status=status)
+    check_weights(r["scores"], idx2.reshape(-1, K), w, ranges(lq), ranges(lk), scores, 1.0, used_q, used_k)
+    assert int(status) == 0
+    sli.key_weights(dev(w).reshape(4, 50, 1, K), dev(idx).reshape(4, 50, 1, K), dev(scores).reshape(4, 400),
+                    seq_used_q=torch.tensor([51, 0, 0, 0], **i32), status=status)
+    assert int(status) == sli.SLIKL_DEV_BAD_SEQ_USED
+
+
+@pytest.mark.parametrize("lk", [300, 60000])
+def test_key_weights_flags(lk):
+    """Indices, weights and cu_seqlens that break the contract are flagged, and touch nothing else."""
+    lq, K = [9, 4], 50
+    idx, w = draw_rows(8, lq, [lk, lk], K, invalid=0.2)
+    scores = torch.zeros(2 * lk)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def run(idx, w, cq=cu(lq), ck=cu([lk, lk])):
+        status.zero_()
+        r = sli.key_weights(dev(w)[:, None], dev(idx)[:, None], dev(scores), layout_q="TND", layout_k="TND",
+                            cu_seqlens_q=dev(cq), cu_seqlens_k=dev(ck), status=status)
+        return r["scores"], int(status)
+
+    for bad in (lk, -2, 2 ** 31 - 1, -2 ** 31):
+        i2 = idx.clone()
+        i2[3, 7] = bad
+        got, st = run(i2, w)
+        assert st == sli.SLIKL_DEV_INDEX_OUT_OF_RANGE
+        i2[3, 7] = -1
+        check_weights(got, i2, w, ranges(lq), ranges([lk, lk]), scores, 1.0)
+    for bad, stands in ((-1.0, 0.0), (float("nan"), 0.0), (2.5, 2.0), (float("inf"), 2.0), (float("-inf"), 0.0)):
+        i2, w2 = idx.clone(), w.clone()
+        i2[3, 7], w2[3, 7] = 5, bad
+        got, st = run(i2, w2)
+        assert st == sli.SLIKL_DEV_BAD_WEIGHT
+        w2[3, 7] = stands
+        check_weights(got, i2, w2, ranges(lq), ranges([lk, lk]), scores, 1.0)
+    i32 = torch.int32
+    for cq, ck, bit in ((torch.tensor([0, 20, 13], dtype=i32), cu([lk, lk]), sli.SLIKL_DEV_BAD_CU_SEQLENS_Q),
+                        (torch.tensor([0, 9, 12], dtype=i32), cu([lk, lk]), sli.SLIKL_DEV_BAD_CU_SEQLENS_Q),
+                        (torch.tensor([-5, 9, 13], dtype=i32), cu([lk, lk]), sli.SLIKL_DEV_BAD_CU_SEQLENS_Q),
+                        (cu(lq), torch.tensor([0, 3 * lk, 2 * lk], dtype=i32), sli.SLIKL_DEV_BAD_CU_SEQLENS_K),
+                        (cu(lq), torch.tensor([-7, lk, 2 * lk], dtype=i32), sli.SLIKL_DEV_BAD_CU_SEQLENS_K)):
+        got, st = run(idx, w, cq, ck)
+        assert st & bit
+
+
+def test_key_weights_beyond_one_pass_of_p():
+    """A hot key that every row names with its whole weight: the sum is exact."""
+    T, S2 = 5000, 40
+    idx = torch.full((1, T, 1, 4), -1, dtype=torch.int32)
+    idx[..., 2] = 17
+    w = torch.full((1, T, 1, 4), 7.0)
+    w[..., 2] = 1.0
+    r = sli.key_weights(dev(w), dev(idx), torch.zeros(1, S2, device="cuda"))["scores"].cpu()
+    assert r[0, 17] == T and r.sum() == T
+
+
+def test_key_weights_without_queries_or_keys():
+    e = torch.empty(0, 1, 8, device="cuda")
+    s = torch.rand(30, device="cuda")
+    z = dev(torch.zeros(2, dtype=torch.int32))
+    r = sli.key_weights(e, e.int(), s, decay=0.5, layout_q="TND", layout_k="TND", cu_seqlens_q=z,
+                        cu_seqlens_k=dev(cu([30])))
+    assert torch.equal(r["scores"], s * 0.5)
+    w = torch.rand(2, 1, 8, device="cuda")
+    r = sli.key_weights(w, torch.full((2, 1, 8), -1, dtype=torch.int32, device="cuda"), s[:0], layout_q="TND",
+                        layout_k="TND", cu_seqlens_q=dev(cu([2])), cu_seqlens_k=z)
+    assert r["scores"].numel() == 0
+
+
+# --- eviction ------------------------------------------------------------------------------------
+
+def make_scores(seed, total, kind):
+    g = torch.Generator().manual_seed(seed)
+    if kind == "normal":
+        return torch.randn(total, generator=g)
+    if kind == "ties":                          # few values, both zeros among them
+        return torch.randint(-2, 3, (total,), generator=g).float() * torch.where(
+            torch.rand(total, generator=g) < 0.5, -1.0, 1.0)
+    if kind == "same":
+        return torch.full((total,), 0.25)
+    if kind == "close":                         # alike in their high bits
+        return 1 + torch.randint(0, 1000, (total,), generator=g).float() * 2.0 ** -23
+    s = torch.randn(total, generator=g) * torch.exp(20 * torch.randn(total, generator=g))
+    r = torch.rand(total, generator=g)
+    for k, v in enumerate((float("nan"), float("inf"), float("-inf"), 0.0, -0.0, 1e-45, -1e-45, -float("nan"))):
+        s[(r >= 0.05 * k) & (r < 0.05 * (k + 1))] = v
+    return s
+
+
+EVICT = [
+    # layout, lengths, budget, sinks, recent
+    ("BSND", [37] * 3, 12, 2, 3),
+    ("BSND", [601], 150, 4, 32),
+    ("BSND", [1024] * 2, 1, 0, 0),
+    ("BSND", [1025] * 2, 1024, 0, 0),
+    ("BSND", [5000] * 4, 700, 700, 0),
+    ("BSND", [5000] * 2, 700, 0, 700),
+    ("BSND", [8192] * 4, 2048, 4, 64),
+    ("BSND", [20000] * 2, 19999, 1, 1),
+    ("BSND", [131072], 16384, 4, 32),
+    ("TND", [0, 1, 5, 900, 40, 33000], 40, 3, 5),
+    ("TND", [50] * 200, 33, 0, 1),
+    ("TND", [140000, 3], 5000, 0, 0),
+]
+
+
+@pytest.mark.parametrize("case", EVICT, ids=lambda c: f"{c[0]}-{len(c[1])}x{max(c[1])}-{c[2]}-{c[3]}-{c[4]}")
+@pytest.mark.parametrize("kind", ["normal", "ties", "same", "close", "strange"])
+def test_evict(case, kind):
+    layout, lens, budget, sinks, recent = case
+    B, total = len(lens), sum(lens)
+    scores = make_scores(11, total, kind)
+    g = torch.Generator().manual_seed(12)
+    bsnd = layout == "BSND"
+    used = [max(0, n - 7 * b) for b, n in enumerate(lens)] if bsnd and B > 2 else None
+    caches = [torch.randn(total, 1, 64, generator=g).to(torch.bfloat16), torch.randn(total, 2, 2, generator=g),
+              torch.randint(0, 255, (total, 48), generator=g).to(torch.uint8)]
+    lead = (B, lens[0]) if bsnd else (total,)
+    outs = [torch.full((B, budget, *c.shape[1:]), 3, dtype=c.dtype, device="cuda") for c in caches]
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    r = sli.evict(dev(scores).reshape(lead), [dev(c).reshape(*lead, *c.shape[1:]) for c in caches], budget, sinks, recent,
+                  layout_k=layout, cu_seqlens_k=None if bsnd else dev(cu(lens)),
+                  seq_used_k=None if used is None else torch.tensor(used, dtype=torch.int32, device="cuda"),
+                  out=dict(caches=outs), status=status)
+    assert int(status) == 0
+    for b, (at, n) in enumerate(ranges(lens)):
+        n = n if used is None else used[b]
+        keep = ref.evict(scores[at: at + n], n, budget, sinks, recent)
+        m = len(keep)
+        assert int(r["lengths"][b]) == m
+        assert r["kept"][b].tolist() == keep + [-1] * (budget - m)
+        rows = at + torch.tensor(keep, dtype=torch.long)
+        got = r["scores"][b].cpu()
+        assert torch.equal(got[:m].view(torch.int32), scores[rows].view(torch.int32)) and (got[m:] == 0).all()
+        for c, o in zip(caches, r["caches"]):
+            assert torch.equal(o[b, :m].cpu(), c[rows]) and (o[b, m:] == 3).all()
+
+
+def test_evict_without_caches_and_default_outputs():
+    s = torch.rand(2, 100, device="cuda")
+    r = sli.evict(s, [], 10)
+    assert r["caches"] == [] and (r["lengths"] == 10).all()
+    c = torch.rand(2, 100, 4, device="cuda")
+    used = torch.tensor([3, 100], dtype=torch.int32, device="cuda")
+    r = sli.evict(s, [c], 10, seq_used_k=used)
+    assert torch.equal(r["caches"][0][0, :3], c[0, :3]) and (r["caches"][0][0, 3:] == 0).all()
+
+
+def test_evict_flags():
+    s = torch.rand(3, 20, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    r = sli.evict(s, [], 30, seq_used_k=torch.tensor([21, -1, 20], dtype=torch.int32, device="cuda"), status=status)
+    assert int(status) == sli.SLIKL_DEV_BAD_SEQ_USED and r["lengths"].tolist() == [20, 0, 20]
+    c = torch.rand(60, 4, device="cuda")
+    for bad in ([0, 70, 60], [0, 30, 20], [-4, 30, 60], [0, 30, 59]):
+        status.zero_()
+        r = sli.evict(s.reshape(-1), [c], 5, layout_k="TND", cu_seqlens_k=torch.tensor(bad, dtype=torch.int32, device="cuda"),
+                      status=status)
+        torch.cuda.synchronize()
+        assert int(status) & sli.SLIKL_DEV_BAD_CU_SEQLENS_K
+
+
+def test_evict_beyond_32_bits():
+    """A cache of more than 2^32 bytes whose last rows stay."""
+    S2, row = 1 << 20, 4352 // 2
+    c = torch.zeros(2, S2, row, dtype=torch.bfloat16, device="cuda")
+    c[1, -3:] = torch.arange(3, device="cuda")[:, None].to(torch.bfloat16) + 1
+    s = torch.zeros(2, S2, device="cuda")
+    s[1, -3:] = 1
+    r = sli.evict(s, [c], 4)
+    assert r["kept"].tolist() == [[0, 1, 2, 3], [0, S2 - 3, S2 - 2, S2 - 1]]
+    assert torch.equal(r["caches"][0][1, 1:], c[1, -3:])
+
+
+# --- together ------------------------------------------------------------------------------------
+
+def test_weights_then_eviction_then_the_gradient_on_the_smaller_cache():
+    """p of grad_recompute_p -> key_weights -> evict -> grad on the smaller cache, whose slots are the
+    kept keys' new places and whose lengths are its used lengths, against the gradient on the full
+    cache with the same keys named."""
+    B, S1, S2, K = 2, 24, 300, 64
+    wl = si.small(seed=81, layout="BSND", B=B, S1=S1, S2=S2, N1=16, D=128, K=K)
+    main = si.main_attention(wl, 16, 128, seed=82)
+    first = sli.grad_recompute_p_workload(wl, main)
+    scores = sli.key_weights(first["p"], dev(wl.idx), torch.zeros(B, S2, device="cuda"))["scores"]
+    want = ref.key_weights(first["p"].cpu().reshape(-1, K), wl.idx.reshape(-1, K), ranges([S1] * B), ranges([S2] * B),
+                           torch.zeros(B * S2), 0.0)
+    assert ((scores.cpu().double().reshape(-1) - want).abs() <= want * 2.0 ** -24 + S1 * 2.0 ** -41).all()
+    assert abs(float(scores.double().sum()) - B * S1) < 1e-2 * B * S1    # each row's p sums to one
+    budget = 100
+    k = dev(wl.k)
+    cut = sli.evict(scores, [k], budget, sinks=2, recent=10)
+    place = torch.full((B, S2), -1, dtype=torch.int32, device="cuda")
+    for b in range(B):
+        place[b, cut["kept"][b].long()] = torch.arange(budget, dtype=torch.int32, device="cuda")
+    idx = dev(wl.idx).reshape(B, -1)
+    new = torch.where(idx >= 0, place.gather(1, idx.clamp_min(0).long()), -1).reshape(wl.idx.shape)
+    full = torch.where(new >= 0, dev(wl.idx), -1)
+    p = torch.where(new >= 0, first["p"], 0.0)
+    p = p / p.sum(-1, keepdim=True).clamp_min(1e-30)
+    args = dev(wl.w), p
+    small = sli.grad(dev(wl.q), cut["caches"][0], *args, new, deterministic=True, seq_used_k=cut["lengths"])
+    big = sli.grad(dev(wl.q), k, *args, full, deterministic=True)
+    torch.cuda.synchronize()
+    assert sli.slikl_read_device_status(small["workspace"].data_ptr()) == 0
+    for n in ("dq", "dw", "softmax_out"):
+        assert torch.equal(small[n], big[n]), n
+    # dk's sums run over other blocks of keys: the same terms, at most S1 * 16 of |w| |q|, in another
+    # order in fp32, then one rounding to 16 bits on either side
+    terms = S1 * 16 * float(wl.w.abs().max()) * float(wl.q.float().abs().max())
+    for b in range(B):
+        x, y = small["dk"][b].float(), big["dk"][b, cut["kept"][b].long()].float()
+        assert ((x - y).abs() <= 2 * 2.0 ** -8 * y.abs() + 2 * S1 * 16 * 2.0 ** -24 * terms).all()
+
+
+def test_graph_and_other_stream():
+    lq, lk, K = [64], [3000], 128
+    idx, w = draw_rows(21, lq, lk, K)
+    i, w, s = dev(idx).reshape(1, 64, 1, K), dev(w).reshape(1, 64, 1, K), torch.rand(1, 3000, device="cuda")
+    c = torch.randn(1, 3000, 64, device="cuda")
+    want = sli.key_weights(w, i, s)["scores"]
+    cut = sli.evict(want, [c], 500, 4, 8)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    a = sli.key_weights(w, i, s, stream=st)["scores"]
+    b = sli.evict(a, [c], 500, 4, 8, stream=st)
+    st.synchronize()
+    assert torch.equal(a, want) and torch.equal(b["kept"], cut["kept"]) and torch.equal(b["caches"][0], cut["caches"][0])
+    ws = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    graphs = []
+    for scale in (1.0, 0.5):                    # two graphs that share one workspace
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            a = sli.key_weights(w * scale, i, s, workspace=ws)["scores"]
+            b = sli.evict(a, [c], 500, 4, 8)
+        graphs.append((g, a, b, scale))
+    for j in (0, 1, 1, 0):
+        graphs[j][0].replay()
+    torch.cuda.synchronize()
+    for _, a, b, scale in graphs:
+        want = sli.key_weights(w * scale, i, s)["scores"]
+        cut = sli.evict(want, [c], 500, 4, 8)
+        assert torch.equal(a, want) and torch.equal(b["kept"], cut["kept"])
+        assert torch.equal(b["caches"][0], cut["caches"][0])
