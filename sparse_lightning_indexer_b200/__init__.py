@@ -10,8 +10,8 @@ sm_100 device is present the calls raise.
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import os
 from typing import NamedTuple, Optional, Sequence
 
@@ -722,40 +722,48 @@ class Checkpoint(NamedTuple):
     dtype: torch.dtype
 
 
-@contextlib.contextmanager
-def _on_stream(device: torch.device, stream):
-    with torch.cuda.device(device):
+def _on_stream(f):
+    """f with its `stream` argument, where one is given, as the current stream: what f allocates
+    then belongs to that stream too."""
+    @functools.wraps(f)
+    def call(*args, stream=None, **kw):
         if stream is None:
-            yield torch.cuda.current_stream(device)
-        else:
-            with torch.cuda.stream(stream):
-                yield stream
+            return f(*args, **kw)
+        with torch.cuda.stream(stream):
+            return f(*args, **kw)
+    return call
 
 
-def _check(t, name, device, dtype, shape=None):
-    """Device address of a contiguous CUDA tensor of this device, type and shape; None for None."""
-    if t is None:
-        return None
-    if t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous tensor on {device}")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+def _launch(index, call, *args):
+    """call(*args, stream) on device `index` and its current stream."""
+    stream = torch._C._cuda_getCurrentRawStream(index)
+    if torch.cuda.current_device() == index:
+        call(*args, stream)
+    else:
+        with torch.cuda.device(index):
+            call(*args, stream)
+
+
+def _at(t, name, index, dtype, shape=None):
+    """Device address of a contiguous tensor of CUDA device `index`, this type and shape."""
+    if (t.get_device() != index or t.dtype is not dtype or not t.is_contiguous()
+            or (shape is not None and t.shape != shape)):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor on cuda:{index}"
+                         + (f" of shape {tuple(shape)}" if shape is not None else "")
+                         + f", not {t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
 def _row_stride(t, name):
     """Elements from one row to the next of t [B, S, N, D] or [T, N, D] whose heads are dense."""
-    shape, st = t.shape, t.stride()
-    N, D = shape[-2], shape[-1]
-    dense = N * D
-    if t.numel() == 0:
+    shape = t.shape
+    dense = shape[-2] * shape[-1]
+    if t.is_contiguous():
         return dense
-    row = dense
-    if st[-1] != 1 or (N > 1 and st[-2] != D):
+    st, row = t.stride(), dense
+    if st[-1] != 1 or (shape[-2] > 1 and st[-2] != shape[-1]):
         raise ValueError(f"{name}: the heads of a row must be contiguous")
-    if t.dim() == 3:
+    if len(shape) == 3:
         if shape[0] > 1:
             row = st[0]
     elif shape[1] > 1:
@@ -769,79 +777,76 @@ def _row_stride(t, name):
     return row
 
 
-def _qk_side(x, name, layout, device, positions, gain, bias, norm, rot):
-    """(side struct, tensor struct with what both directions read, shape, dtype) of x or its
-    Checkpoint; x None = no such side."""
-    if norm not in _NORMS:
-        raise ValueError(f"norm_{name} must be one of {sorted(_NORMS)}")
-    kind = _NORMS[norm]
-    side, tn = slikl_qk_side(0, 1, 1, 0, 0, kind, 0), slikl_qk_side_tensors()
-    if x is None:
-        return side, tn, None, None
-    src = x.values if isinstance(x, Checkpoint) else x
-    shape, D = src.shape, src.shape[-1]
-    if src.device != device or len(shape) != (4 if layout == "BSND" else 3):
-        raise ValueError(f"x_{name}: {layout} rows on {device} are wanted")
-    if isinstance(x, Checkpoint):
-        dtype = x.dtype
-        tn.x8 = _check(x.values, f"x_{name}.values", device, torch.float8_e4m3fn)
-        tn.x8_scale = _check(x.scale, f"x_{name}.scale", device, torch.float32, shape[:-1])
+def _qk_side(side, tn, x, name, layout, index, D, dtype, rot, positions, gain, bias, norm):
+    """Enters one side, x or its Checkpoint, with what both directions read of it; returns its shape."""
+    if norm not in _NORMS or layout not in _LAYOUTS:
+        raise ValueError(f"norm_{name} must be one of {sorted(_NORMS)}, layout_{name} of {sorted(_LAYOUTS)}")
+    if type(x) is Checkpoint:
+        shape = x.values.shape
+        tn.x8 = _at(x.values, f"x_{name}.values", index, torch.float8_e4m3fn)
+        tn.x8_scale = _at(x.scale, f"x_{name}.scale", index, torch.float32, shape[:-1])
     else:
-        dtype = x.dtype
-        side.x_stride = _row_stride(x, f"x_{name}")
+        shape = x.shape
+        if x.get_device() != index:
+            raise ValueError(f"x_{name} must be on cuda:{index}")
         tn.x = x.data_ptr()
-    side.N = shape[-2]
-    side.T = shape[0] * shape[1] if layout == "BSND" else shape[0]
-    if layout == "BSND":
-        side.S = max(1, shape[1])
-    elif positions is None and rot and side.T:
+    bsnd = layout == "BSND"
+    if len(shape) != (4 if bsnd else 3) or shape[-1] != D or x.dtype is not dtype:
+        raise ValueError("q and k must be BSND or TND rows that share D and one dtype, float16 or bfloat16")
+    if type(x) is not Checkpoint:
+        side.x_stride = _row_stride(x, f"x_{name}")
+    side.N, side.norm = shape[-2], _NORMS[norm]
+    side.T = T = shape[0] * shape[1] if bsnd else shape[0]
+    side.S = max(1, shape[1]) if bsnd else 1
+    if positions is not None:
+        tn.positions = _at(positions, f"pos_{name}", index, torch.int32)
+        if positions.numel() != T:
+            raise ValueError(f"pos_{name} must have {T} entries")
+    elif rot and T and not bsnd:
         raise ValueError(f"TND needs pos_{name}")
-    tn.positions = _check(positions, f"pos_{name}", device, torch.int32)
-    if positions is not None and positions.numel() != side.T:
-        raise ValueError(f"pos_{name} must have {side.T} entries")
-    tn.gain = _check(gain, f"gain_{name}", device, torch.float32, (D,))
-    tn.bias = _check(bias, f"bias_{name}", device, torch.float32, (D,))
-    return side, tn, shape, dtype
+    if gain is not None:
+        tn.gain = _at(gain, f"gain_{name}", index, torch.float32, (D,))
+    if bias is not None:
+        tn.bias = _at(bias, f"bias_{name}", index, torch.float32, (D,))
+    return shape
 
 
-def _qk_call(x_q, x_k, cos_sin, pos, gain, bias, norm, rot_layout, eps, layouts, status):
-    """(problem, tensors, [(shape, dtype) of q, k], device) of either direction."""
+def _qk_call(x_q, x_k, cos_sin, pos_q, pos_k, gain_q, gain_k, bias_q, bias_k, norm_q, norm_k,
+             rot_layout, eps, layout_q, layout_k, status):
+    """(problem, tensors, shape of q, of k, dtype, device index) of either direction; the shape of a
+    side that is None is None."""
     some = x_q if x_q is not None else x_k
     if some is None:
         raise ValueError("x_q and x_k are both None")
-    device = (some.values if isinstance(some, Checkpoint) else some).device
-    if device.type != "cuda":
-        raise ValueError("tensors must be CUDA tensors")
-    if rot_layout not in _ROTS:
-        raise ValueError(f"rot_layout must be one of {sorted(_ROTS)}")
-    rot = 0 if cos_sin is None else cos_sin.shape[-1]
-    pr, tn, said = slikl_qk_problem(), slikl_qk_tensors(), []
-    for i, (name, x) in enumerate((("q", x_q), ("k", x_k))):
-        if layouts[i] not in _LAYOUTS:
-            raise ValueError(f"layout_{name} must be one of {sorted(_LAYOUTS)}")
-        side, t, shape, dtype = _qk_side(x, name, layouts[i], device, pos[i], gain[i], bias[i],
-                                         norm[i], rot)
-        setattr(pr, name, side)
-        setattr(tn, name, t)
-        said.append((shape, dtype))
-    (sq, dq), (sk, dk) = said
-    dtype, D = (dq, sq[-1]) if sq is not None else (dk, sk[-1])
-    if dtype not in _DT or (sq is not None and sk is not None and (dk != dtype or sk[-1] != D)):
-        raise ValueError("q and k must share D and one dtype, float16 or bfloat16")
-    pr.dtype, pr.rot_layout, pr.D, pr.rot_dim, pr.eps = _DT[dtype], _ROTS[rot_layout], D, rot, eps
+    values, dtype = (some.values if type(some) is Checkpoint else some), some.dtype
+    index, D = values.get_device(), values.shape[-1]
+    if index < 0 or dtype not in _DT or rot_layout not in _ROTS:
+        raise ValueError("CUDA tensors of float16 or bfloat16 and rot_layout halves or pairs are wanted")
+    rot = 0
+    pr, tn = slikl_qk_problem(), slikl_qk_tensors()
     if cos_sin is not None:
-        if cos_sin.dim() != 2:
-            raise ValueError("cos_sin must be [positions, rotated dims]")
-        pr.table_rows = cos_sin.shape[0]
-        tn.cos_sin = _check(cos_sin, "cos_sin", device, torch.float32)
-    tn.status = _check(status, "status", device, torch.int32, (1,))
-    return pr, tn, said, device
+        pr.table_rows, rot = cos_sin.shape
+        tn.cos_sin = _at(cos_sin, "cos_sin", index, torch.float32)
+    pr.dtype, pr.rot_layout, pr.D, pr.rot_dim, pr.eps = _DT[dtype], _ROTS[rot_layout], D, rot, eps
+    shape_q = shape_k = None
+    if x_q is not None:
+        shape_q = _qk_side(pr.q, tn.q, x_q, "q", layout_q, index, D, dtype, rot, pos_q, gain_q, bias_q, norm_q)
+    else:
+        pr.q.N = 1
+    if x_k is not None:
+        shape_k = _qk_side(pr.k, tn.k, x_k, "k", layout_k, index, D, dtype, rot, pos_k, gain_k, bias_k, norm_k)
+    else:
+        pr.k.N = 1
+    if status is not None:
+        tn.status = _at(status, "status", index, torch.int32, (1,))
+    return pr, tn, shape_q, shape_k, dtype, index
 
 
+@_on_stream
 def qk_norm_rope(x_q, x_k, cos_sin=None, *, pos_q=None, pos_k=None, gain_q=None, gain_k=None,
                  bias_q=None, bias_k=None, norm_q="rms", norm_k="rms", rot_layout="halves",
                  eps=1e-6, layout_q="BSND", layout_k="BSND", checkpoint=False, out=None,
-                 status=None, stream=None):
+                 status=None):
     """q and k of the indexer from the outputs of their projections (slikl_qk_norm_rope).
 
     x_q [B,S1,N1,D] / [T1,N1,D], x_k [B,S2,N2,D] / [T2,N2,D] in float16 or bfloat16, or a
@@ -850,170 +855,181 @@ def qk_norm_rope(x_q, x_k, cos_sin=None, *, pos_q=None, pos_k=None, gain_q=None,
     `cos_sin` fp32 [positions, R] holds the cosines of a position's R/2 angles, then the sines (None:
     no rotation); `rot_layout` "halves" turns dims (i, i + R/2), "pairs" (2i, 2i + 1). `pos_*` are
     int32 positions per row (-1: padding row, all zero); without them a BSND row stands at its place
-    in its batch. `status` (int32 [1]) receives SLIKL_DEV_BAD_POSITION.
+    in its batch. `status` (int32 [1]) receives SLIKL_DEV_BAD_POSITION. `stream`: as the current one.
     Returns dict(q, k) and, with checkpoint=True, checkpoint_q / checkpoint_k; `out` may supply q, k.
     """
-    pr, tn, said, device = _qk_call(x_q, x_k, cos_sin, (pos_q, pos_k), (gain_q, gain_k),
-                                    (bias_q, bias_k), (norm_q, norm_k), rot_layout, eps,
-                                    (layout_q, layout_k), status)
-    res = {}
-    with _on_stream(device, stream) as s:
-        for name, (shape, dtype), t in (("q", said[0], tn.q), ("k", said[1], tn.k)):
-            y = out.get(name) if out else None
-            if y is None and shape is not None:
-                y = torch.empty(shape, dtype=dtype, device=device)
-            res[name] = y
-            if shape is None:
-                continue
-            t.y = _check(y, name, device, dtype, shape)
-            if checkpoint:
-                c = Checkpoint(torch.empty(shape, dtype=torch.float8_e4m3fn, device=device),
-                               torch.empty(shape[:-1], dtype=torch.float32, device=device), dtype)
-                t.keep8, t.keep8_scale = c.values.data_ptr(), c.scale.data_ptr()
-                res["checkpoint_" + name] = c
-        slikl_qk_norm_rope(pr, tn, s.cuda_stream)
+    pr, tn, shape_q, shape_k, dtype, index = _qk_call(
+        x_q, x_k, cos_sin, pos_q, pos_k, gain_q, gain_k, bias_q, bias_k, norm_q, norm_k, rot_layout,
+        eps, layout_q, layout_k, status)
+    res = dict(q=None, k=None)
+    for name, shape, t in (("q", shape_q, tn.q), ("k", shape_k, tn.k)):
+        if shape is None:
+            continue
+        y = out.get(name) if out else None
+        if y is None:
+            y = torch.empty(shape, dtype=dtype, device=index)
+            t.y = y.data_ptr()
+        else:
+            t.y = _at(y, name, index, dtype, shape)
+        res[name] = y
+        if checkpoint:
+            c = Checkpoint(torch.empty(shape, dtype=torch.float8_e4m3fn, device=index),
+                           torch.empty(shape[:-1], dtype=torch.float32, device=index), dtype)
+            t.keep8, t.keep8_scale = c.values.data_ptr(), c.scale.data_ptr()
+            res["checkpoint_" + name] = c
+    _launch(index, slikl_qk_norm_rope, pr, tn)
     return res
 
 
+@_on_stream
 def qk_norm_rope_grad(dq, dk, x_q, x_k, cos_sin=None, *, pos_q=None, pos_k=None, gain_q=None,
                       gain_k=None, norm_q="rms", norm_k="rms", rot_layout="halves", eps=1e-6,
-                      layout_q="BSND", layout_k="BSND", out=None, workspace=None, status=None,
-                      stream=None):
+                      layout_q="BSND", layout_k="BSND", out=None, workspace=None, status=None):
     """The gradient of qk_norm_rope at x (or its Checkpoint): dq, dk as grad() returns them back to
     the projections. Returns dict(dx_q, dx_k, dgain_q, dgain_k, dbias_q, dbias_k, workspace); a
     side without a norm has no dgain, one without a layer norm no dbias. `out` may supply
     dx_q / dx_k, whose rows may lie apart (slices of one projection's gradient)."""
-    pr, tn, said, device = _qk_call(x_q, x_k, cos_sin, (pos_q, pos_k), (gain_q, gain_k),
-                                    (None, None), (norm_q, norm_k), rot_layout, eps,
-                                    (layout_q, layout_k), status)
-    with _on_stream(device, stream) as s:
-        res = _qk_gradients(pr, tn, said, device, out)
-        for name, dy, (shape, dtype), t in (("dq", dq, said[0], tn.q), ("dk", dk, said[1], tn.k)):
-            if shape is not None:
-                if dy is None:
-                    raise ValueError(f"{name} is missing")
-                t.dy = _check(dy, name, device, dtype, shape)
-        nbytes = slikl_qk_norm_rope_grad_workspace_size(pr)
-        if workspace is None or workspace.numel() < nbytes:
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
-        slikl_qk_norm_rope_grad(pr, tn, workspace.data_ptr(), workspace.numel(), s.cuda_stream)
+    pr, tn, shape_q, shape_k, dtype, index = _qk_call(
+        x_q, x_k, cos_sin, pos_q, pos_k, gain_q, gain_k, None, None, norm_q, norm_k, rot_layout, eps,
+        layout_q, layout_k, status)
+    for name, dy, shape, t in (("dq", dq, shape_q, tn.q), ("dk", dk, shape_k, tn.k)):
+        if shape is not None:
+            if dy is None:
+                raise ValueError(f"{name} is missing")
+            t.dy = _at(dy, name, index, dtype, shape)
+    res = _qk_gradients(pr, tn, shape_q, shape_k, dtype, index, out)
+    nbytes = slikl_qk_norm_rope_grad_workspace_size(pr)
+    if workspace is None or workspace.numel() < nbytes:
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=index)
+    _launch(index, slikl_qk_norm_rope_grad, pr, tn, workspace.data_ptr(), workspace.numel())
     res["workspace"] = workspace
     return res
 
 
-def _qk_gradients(pr, tn, said, device, out):
+def _qk_gradients(pr, tn, shape_q, shape_k, dtype, index, out):
     """Allocates (or takes from `out`) dx, dgain and dbias and enters them in the structs."""
-    res = {}
-    for name, (shape, dtype), side, t in (("q", said[0], pr.q, tn.q), ("k", said[1], pr.k, tn.k)):
-        dx = out.get("dx_" + name) if out else None
-        res["dx_" + name] = res["dgain_" + name] = res["dbias_" + name] = None
+    res = dict(dx_q=None, dx_k=None, dgain_q=None, dgain_k=None, dbias_q=None, dbias_k=None)
+    # the sums of a side are the rows of one tensor
+    norm_q = pr.q.norm if shape_q is not None else 0
+    norm_k = pr.k.norm if shape_k is not None else 0
+    sums = []
+    if norm_q or norm_k:
+        sums = list(torch.empty((norm_q + norm_k, pr.D), dtype=torch.float32, device=index).unbind(0))
+    for name, shape, side, t, norm in (("q", shape_q, pr.q, tn.q, norm_q), ("k", shape_k, pr.k, tn.k, norm_k)):
         if shape is None:
             continue
+        dx = out.get("dx_" + name) if out else None
         if dx is None:
-            dx = torch.empty(shape, dtype=dtype, device=device)
-        elif dx.device != device or dx.dtype != dtype or dx.shape != shape:
-            raise ValueError(f"dx_{name} must be {dtype} {tuple(shape)} on {device}")
-        side.dx_stride = _row_stride(dx, f"dx_{name}")
+            dx = torch.empty(shape, dtype=dtype, device=index)
+        elif dx.get_device() != index or dx.dtype is not dtype or dx.shape != shape:
+            raise ValueError(f"dx_{name} must be {dtype} {tuple(shape)} on cuda:{index}")
+        else:
+            side.dx_stride = _row_stride(dx, f"dx_{name}")
         t.dx = dx.data_ptr()
         res["dx_" + name] = dx
-        for what, least in (("dgain", SLIKL_NORM_RMS), ("dbias", SLIKL_NORM_LAYER)):
-            if side.norm >= least:
-                g = torch.empty(shape[-1], dtype=torch.float32, device=device)
-                setattr(t, what, g.data_ptr())
-                res[f"{what}_{name}"] = g
+        if norm >= SLIKL_NORM_RMS:
+            g = res["dgain_" + name] = sums.pop()
+            t.dgain = g.data_ptr()
+        if norm == SLIKL_NORM_LAYER:
+            g = res["dbias_" + name] = sums.pop()
+            t.dbias = g.data_ptr()
     return res
 
 
-def checkpoint_pack(x, stream=None) -> Checkpoint:
-    """8-bit checkpoint of x [.., N, D] (float16 or bfloat16, rows contiguous, D 64 or 128): one
-    e4m3 value an element and one fp32 scale, max|x| / 448, for each of the D-long rows."""
-    D = x.shape[-1]
-    if x.device.type != "cuda" or not x.is_contiguous() or x.dtype not in _DT:
-        raise ValueError("x must be a contiguous CUDA tensor of float16 or bfloat16")
-    rows = x.numel() // D if D else 0
-    pr, tn = _rows_problem(rows, D, x.dtype)
-    with _on_stream(x.device, stream) as s:
-        c = Checkpoint(torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device),
-                       torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device), x.dtype)
-        tn.q.x, tn.q.keep8, tn.q.keep8_scale = x.data_ptr(), c.values.data_ptr(), c.scale.data_ptr()
-        slikl_qk_norm_rope(pr, tn, s.cuda_stream)
+@_on_stream
+def checkpoint_pack(x) -> Checkpoint:
+    """8-bit checkpoint of x [.., N, D] (float16 or bfloat16, contiguous, D 64 or 128): one e4m3
+    value an element and one fp32 scale, max|x| / 448, for each of the D-long rows."""
+    index = x.get_device()
+    if index < 0:
+        raise ValueError("x must be a CUDA tensor")
+    pr, tn = _rows_problem(x, x.dtype)
+    c = Checkpoint(torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=index),
+                   torch.empty(x.shape[:-1], dtype=torch.float32, device=index), x.dtype)
+    tn.q.x = _at(x, "x", index, x.dtype)
+    tn.q.keep8, tn.q.keep8_scale = c.values.data_ptr(), c.scale.data_ptr()
+    _launch(index, slikl_qk_norm_rope, pr, tn)
     return c
 
 
-def checkpoint_unpack(c: Checkpoint, stream=None) -> torch.Tensor:
+@_on_stream
+def checkpoint_unpack(c: Checkpoint) -> torch.Tensor:
     """The tensor that a checkpoint stands for, scale * values rounded to its 16-bit type."""
-    v, D = c.values, c.values.shape[-1]
-    if v.device.type != "cuda":
+    index = c.values.get_device()
+    if index < 0:
         raise ValueError("tensors must be CUDA tensors")
-    pr, tn = _rows_problem(v.numel() // D if D else 0, D, c.dtype)
-    tn.q.x8 = _check(v, "values", v.device, torch.float8_e4m3fn)
-    tn.q.x8_scale = _check(c.scale, "scale", v.device, torch.float32, v.shape[:-1])
-    with _on_stream(v.device, stream) as s:
-        x = torch.empty(v.shape, dtype=c.dtype, device=v.device)
-        tn.q.y = x.data_ptr()
-        slikl_qk_norm_rope(pr, tn, s.cuda_stream)
+    pr, tn = _rows_problem(c.values, c.dtype)
+    tn.q.x8 = _at(c.values, "values", index, torch.float8_e4m3fn)
+    tn.q.x8_scale = _at(c.scale, "scale", index, torch.float32, c.values.shape[:-1])
+    x = torch.empty(c.values.shape, dtype=c.dtype, device=index)
+    tn.q.y = x.data_ptr()
+    _launch(index, slikl_qk_norm_rope, pr, tn)
     return x
 
 
-def _rows_problem(rows, D, dtype):
-    """A problem of D-long rows as they are: neither norm nor rotation."""
-    if dtype not in _DT:
-        raise ValueError("float16 or bfloat16 is wanted")
-    none = slikl_qk_side(0, 1, 1, 0, 0, SLIKL_NORM_NONE, 0)
+def _rows_problem(t, dtype):
+    """A problem of t's D-long rows as they are: neither norm nor rotation."""
+    if dtype not in _DT or t.dim() < 2:
+        raise ValueError("float16 or bfloat16 [.., N, D] is wanted")
+    D = t.shape[-1]
     return (slikl_qk_problem(_DT[dtype], SLIKL_ROT_HALVES, D, 0, 0, 1.0, 0,
-                             slikl_qk_side(rows, 1, 1, 0, 0, SLIKL_NORM_NONE, 0), none),
+                             slikl_qk_side(t.numel() // max(D, 1), 1, 1, 0, 0, SLIKL_NORM_NONE, 0),
+                             slikl_qk_side(0, 1, 1, 0, 0, SLIKL_NORM_NONE, 0)),
             slikl_qk_tensors())
 
 
+@_on_stream
 def grad_projected(x_q, x_k, w, attn_softmax_l1norm, sparse_indices, cos_sin=None, *, pos_q=None,
                    pos_k=None, gain_q=None, gain_k=None, bias_q=None, bias_k=None, norm_q="rms",
                    norm_k="rms", rot_layout="halves", eps=1e-6, layout_q="BSND", layout_k="BSND",
-                   cu_seqlens_q=None, cu_seqlens_k=None, deterministic=False, stream=None, out=None,
+                   cu_seqlens_q=None, cu_seqlens_k=None, deterministic=False, out=None,
                    workspace=None, dk_path="auto", key_range_bound=0, loss=False, seq_used_q=None,
                    seq_used_k=None):
     """grad() from the outputs of the projections, or from their checkpoints: q and k as
     qk_norm_rope forms them, the indexer's gradient, and dq, dk back as qk_norm_rope_grad takes
     them, in one call (slikl_grad_projected). Returns dict(dx_q, dx_k, dgain_*, dbias_*, dw,
     softmax_out, workspace[, loss]); `out` may supply dx_q / dx_k."""
-    qk, qt, said, device = _qk_call(x_q, x_k, cos_sin, (pos_q, pos_k), (gain_q, gain_k),
-                                    (bias_q, bias_k), (norm_q, norm_k), rot_layout, eps,
-                                    (layout_q, layout_k), None)
     if x_q is None or x_k is None:
         raise ValueError("x_q and x_k are both needed")
-    (sq, dtype), (sk, _) = said
-    pr = slikl_problem(_DT[dtype], _LAYOUTS[layout_q], _LAYOUTS[layout_k],
-                       1 if deterministic else 0)
+    qk, qt, sq, sk, dtype, index = _qk_call(
+        x_q, x_k, cos_sin, pos_q, pos_k, gain_q, gain_k, bias_q, bias_k, norm_q, norm_k, rot_layout,
+        eps, layout_q, layout_k, None)
+    i32, f32 = torch.int32, torch.float32
+    pr = slikl_problem(_DT[dtype], _LAYOUTS[layout_q], _LAYOUTS[layout_k], 1 if deterministic else 0)
     pr.T1, pr.T2, pr.N1, pr.D, pr.topk = qk.q.T, qk.k.T, sq[-2], sq[-1], sparse_indices.shape[-1]
     pr.B = _batches(layout_q, layout_k, sq[0], sk[0], cu_seqlens_q, cu_seqlens_k)
     if layout_q == "BSND":
         pr.S1 = sq[1]
     pr.S2 = sk[1] if layout_k == "BSND" else int(key_range_bound)
-    i32, f32 = torch.int32, torch.float32
     slots = tuple(sq[:-2]) + (1, pr.topk)
-    with _on_stream(device, stream) as s:
-        res = _qk_gradients(qk, qt, said, device, out)
-        res["dw"] = torch.empty(sq[:-1], dtype=f32, device=device)
-        res["softmax_out"] = torch.empty(slots, dtype=f32, device=device)
-        loss_t = torch.empty(pr.T1, dtype=f32, device=device) if loss else None
-        opt = slikl_options(_DK_PATHS[dk_path], None, None, None, None,
-                            loss_t.data_ptr() if loss else None,
-                            _check(seq_used_q, "seq_used_q", device, i32, (pr.B,)),
-                            _check(seq_used_k, "seq_used_k", device, i32, (pr.B,)))
-        tn = slikl_tensors(
-            None, None, _check(w, "w", device, f32, sq[:-1]),
-            _check(attn_softmax_l1norm, "attn_softmax_l1norm", device, f32, slots),
-            _check(sparse_indices, "sparse_indices", device, i32, slots),
-            _check(cu_seqlens_q, "cu_seqlens_q", device, i32) if layout_q == "TND" else None,
-            _check(cu_seqlens_k, "cu_seqlens_k", device, i32) if layout_k == "TND" else None,
-            None, None, res["dw"].data_ptr(), res["softmax_out"].data_ptr())
-        nbytes = slikl_grad_projected_workspace_size(pr, qk, opt)
-        if workspace is None or workspace.numel() < nbytes:
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
-        slikl_grad_projected(pr, qk, tn, qt, workspace.data_ptr(), workspace.numel(),
-                             s.cuda_stream, opt)
-    res["workspace"] = workspace
+    tn = slikl_tensors()
+    tn.w = _at(w, "w", index, f32, sq[:-1])
+    tn.attn_softmax_l1norm = _at(attn_softmax_l1norm, "attn_softmax_l1norm", index, f32, slots)
+    tn.sparse_indices = _at(sparse_indices, "sparse_indices", index, i32, slots)
+    if layout_q == "TND":
+        tn.cu_seqlens_q = _at(cu_seqlens_q, "cu_seqlens_q", index, i32)
+    if layout_k == "TND":
+        tn.cu_seqlens_k = _at(cu_seqlens_k, "cu_seqlens_k", index, i32)
+    opt = make_options(dk_path)
+    if seq_used_q is not None:
+        opt.seq_used_q = _at(seq_used_q, "seq_used_q", index, i32, (pr.B,))
+    if seq_used_k is not None:
+        opt.seq_used_k = _at(seq_used_k, "seq_used_k", index, i32, (pr.B,))
+    res = _qk_gradients(qk, qt, sq, sk, dtype, index, out)
+    res["dw"] = torch.empty(sq[:-1], dtype=f32, device=index)
+    res["softmax_out"] = torch.empty(slots, dtype=f32, device=index)
+    tn.dw, tn.softmax_out = res["dw"].data_ptr(), res["softmax_out"].data_ptr()
     if loss:
-        res["loss"] = loss_t
+        res["loss"] = torch.empty(pr.T1, dtype=f32, device=index)
+        opt.loss = res["loss"].data_ptr()
+    nbytes = slikl_grad_projected_workspace_size(pr, qk, opt)
+    if workspace is None or workspace.numel() < nbytes:
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=index)
+
+    def call(stream):
+        slikl_grad_projected(pr, qk, tn, qt, workspace.data_ptr(), workspace.numel(), stream, opt)
+    _launch(index, call)
+    res["workspace"] = workspace
     return res
 
 
@@ -1053,56 +1069,62 @@ def slikl_evict(problem: slikl_evict_problem, tensors: slikl_evict_tensors,
         raise SliklError(rc, "slikl_evict")
 
 
-def key_weights(weights, sparse_indices, scores, decay=1.0, layout_q="BSND", layout_k="BSND",
+@_on_stream
+def key_weights(weights, sparse_indices, scores, *, decay=1.0, layout_q="BSND", layout_k="BSND",
                 cu_seqlens_q=None, cu_seqlens_k=None, seq_used_q=None, seq_used_k=None,
-                key_range_bound=0, out=None, workspace=None, status=None, stream=None):
+                key_range_bound=0, out=None, workspace=None, status=None):
     """decay * scores plus, for every key row, the weights of the slots that name it
     (slikl_key_weights): fp32 `weights` and int32 `sparse_indices` [B,S1,1,topk] / [T1,1,topk] (p of
     grad(), softmax_out, or p of grad_recompute_p), fp32 `scores` [B,S2] / [T2]. `out` may be
     `scores`. `status` (int32 [1]) receives the device flags. Returns dict(scores, workspace)."""
-    device, i32, f32 = scores.device, torch.int32, torch.float32
-    if device.type != "cuda" or layout_q not in _LAYOUTS or layout_k not in _LAYOUTS:
+    index, i32, f32 = scores.get_device(), torch.int32, torch.float32
+    if index < 0 or layout_q not in _LAYOUTS or layout_k not in _LAYOUTS:
         raise ValueError("CUDA tensors and layouts BSND or TND are wanted")
-    shape = sparse_indices.shape
+    shape, rows = sparse_indices.shape, scores.shape
     if len(shape) != (4 if layout_q == "BSND" else 3) or shape[-2] != 1 or \
-            scores.dim() != (2 if layout_k == "BSND" else 1):
+            len(rows) != (2 if layout_k == "BSND" else 1):
         raise ValueError("sparse_indices must be [B,S1,1,topk] / [T1,1,topk], scores [B,S2] / [T2]")
-    pr = slikl_problem(SLIKL_BF16, _LAYOUTS[layout_q], _LAYOUTS[layout_k], 0, 0, 0, 0, 0, 0, 1, 64,
-                       shape[-1])
-    pr.B = _batches(layout_q, layout_k, shape[0], scores.shape[0], cu_seqlens_q, cu_seqlens_k)
+    pr, tn = slikl_problem(), slikl_key_weights_tensors()
+    pr.topk = shape[-1]
+    pr.B = _batches(layout_q, layout_k, shape[0], rows[0], cu_seqlens_q, cu_seqlens_k)
     if layout_q == "BSND":
         pr.S1 = shape[1]
     else:
-        pr.T1 = shape[0]
+        pr.layout_q, pr.T1 = SLIKL_TND, shape[0]
+        tn.cu_seqlens_q = _at(cu_seqlens_q, "cu_seqlens_q", index, i32)
     if layout_k == "BSND":
-        pr.S2 = scores.shape[1]
+        pr.S2 = rows[1]
     else:
-        pr.T2, pr.S2 = scores.shape[0], int(key_range_bound)
+        pr.layout_k, pr.T2, pr.S2 = SLIKL_TND, rows[0], int(key_range_bound)
+        tn.cu_seqlens_k = _at(cu_seqlens_k, "cu_seqlens_k", index, i32)
     opt = None
     if seq_used_q is not None or seq_used_k is not None:
-        opt = slikl_options(0, None, None, None, None, None,
-                            _check(seq_used_q, "seq_used_q", device, i32, (pr.B,)),
-                            _check(seq_used_k, "seq_used_k", device, i32, (pr.B,)))
-    with _on_stream(device, stream) as s:
-        if out is None:
-            out = torch.empty_like(scores)
-        tn = slikl_key_weights_tensors(
-            _check(sparse_indices, "sparse_indices", device, i32),
-            _check(weights, "weights", device, f32, shape),
-            _check(cu_seqlens_q, "cu_seqlens_q", device, i32) if layout_q == "TND" else None,
-            _check(cu_seqlens_k, "cu_seqlens_k", device, i32) if layout_k == "TND" else None,
-            _check(scores, "scores", device, f32), _check(out, "out", device, f32, scores.shape),
-            _check(status, "status", device, i32, (1,)))
-        nbytes = slikl_key_weights_workspace_size(pr)
-        if workspace is None or workspace.numel() < nbytes:
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
-        slikl_key_weights(pr, tn, decay, workspace.data_ptr(), workspace.numel(), s.cuda_stream, opt)
+        opt = slikl_options()
+        if seq_used_q is not None:
+            opt.seq_used_q = _at(seq_used_q, "seq_used_q", index, i32, (pr.B,))
+        if seq_used_k is not None:
+            opt.seq_used_k = _at(seq_used_k, "seq_used_k", index, i32, (pr.B,))
+    tn.sparse_indices = _at(sparse_indices, "sparse_indices", index, i32)
+    tn.weights = _at(weights, "weights", index, f32, shape)
+    tn.scores = _at(scores, "scores", index, f32)
+    if status is not None:
+        tn.status = _at(status, "status", index, i32, (1,))
+    if out is None:
+        out = torch.empty_like(scores)
+    tn.out = _at(out, "out", index, f32, rows)
+    nbytes = slikl_key_weights_workspace_size(pr)
+    if workspace is None or workspace.numel() < nbytes:
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=index)
+
+    def call(stream):
+        slikl_key_weights(pr, tn, decay, workspace.data_ptr(), workspace.numel(), stream, opt)
+    _launch(index, call)
     return dict(scores=out, workspace=workspace)
 
 
-def evict(scores, caches: Sequence[torch.Tensor], budget, sinks=0, recent=0, layout_k="BSND",
-          cu_seqlens_k=None, seq_used_k=None, key_range_bound=0, out=None, status=None,
-          stream=None):
+@_on_stream
+def evict(scores, caches: Sequence[torch.Tensor], budget, *, sinks=0, recent=0, layout_k="BSND",
+          cu_seqlens_k=None, seq_used_k=None, key_range_bound=0, out=None, status=None):
     """Cuts a cache to at most `budget` key rows a sequence (slikl_evict): the first `sinks`, the
     last `recent` and those with the highest fp32 `scores` [B,S2] / [T2]. `caches` are up to eight
     tensors [B,S2,..] / [T2,..] of any type whose rows (a multiple of 16 bytes) go along.
@@ -1110,50 +1132,49 @@ def evict(scores, caches: Sequence[torch.Tensor], budget, sinks=0, recent=0, lay
     rows kept [B] (the seq_used_k of the result), their scores, and the caches [B,budget,..].
     `out` may supply any of the four; rows of its caches behind the last kept one are left as they
     were (without it they are zero)."""
-    device, i32, f32 = scores.device, torch.int32, torch.float32
-    if device.type != "cuda" or layout_k not in _LAYOUTS:
+    index, i32, f32 = scores.get_device(), torch.int32, torch.float32
+    if index < 0 or layout_k not in _LAYOUTS:
         raise ValueError("CUDA tensors and layout BSND or TND are wanted")
-    bsnd = layout_k == "BSND"
-    if scores.dim() != (2 if bsnd else 1) or (not bsnd and cu_seqlens_k is None):
+    rows, bsnd = scores.shape, layout_k == "BSND"
+    lead = len(rows)
+    if lead != (2 if bsnd else 1) or (not bsnd and cu_seqlens_k is None):
         raise ValueError("scores must be [B,S2], or [T2] with cu_seqlens_k")
-    if len(caches) > SLIKL_EVICT_MAX_CACHES:
-        raise ValueError(f"at most {SLIKL_EVICT_MAX_CACHES} caches")
-    budget, lead = int(budget), scores.dim()
-    B = scores.shape[0] if bsnd else cu_seqlens_k.numel() - 1
-    pr = slikl_evict_problem(_LAYOUTS[layout_k], len(caches), B,
-                             scores.shape[1] if bsnd else int(key_range_bound),
-                             0 if bsnd else scores.shape[0], budget, int(sinks), int(recent))
-    if budget < 1:
-        raise ValueError("budget must be at least 1")
-    out = out or {}
-    with _on_stream(device, stream) as s:
-        kept, lengths, new = out.get("kept"), out.get("lengths"), out.get("scores")
-        if kept is None:
-            kept = torch.empty(B, budget, dtype=i32, device=device)
-        if lengths is None:
-            lengths = torch.empty(B, dtype=i32, device=device)
-        if new is None:
-            new = torch.empty(B, budget, dtype=f32, device=device)
-        outs = out.get("caches")
-        if outs is None:
-            outs = [torch.zeros(B, budget, *c.shape[lead:], dtype=c.dtype, device=device)
-                    for c in caches]
-        if len(outs) != len(caches):
-            raise ValueError("out['caches'] must have a tensor for each cache")
-        tn = slikl_evict_tensors(
-            _check(scores, "scores", device, f32),
-            None if bsnd else _check(cu_seqlens_k, "cu_seqlens_k", device, i32),
-            _check(seq_used_k, "seq_used_k", device, i32, (B,)),
-            _check(kept, "kept", device, i32, (B, budget)),
-            _check(lengths, "lengths", device, i32, (B,)),
-            _check(new, "scores (out)", device, f32, (B, budget)),
-            _check(status, "status", device, i32, (1,)))
-        for i, (c, o) in enumerate(zip(caches, outs)):
-            rest = c.shape[lead:]
-            if c.shape[:lead] != scores.shape:
-                raise ValueError(f"cache {i} must have scores' rows")
-            tn.caches[i] = (_check(c, f"cache {i}", device, c.dtype),
-                            _check(o, f"out cache {i}", device, c.dtype, (B, budget, *rest)),
-                            rest.numel() * c.element_size())
-        slikl_evict(pr, tn, s.cuda_stream)
-    return dict(kept=kept, lengths=lengths, scores=new, caches=list(outs))
+    if budget < 1 or len(caches) > SLIKL_EVICT_MAX_CACHES:
+        raise ValueError(f"budget must be at least 1, and caches at most {SLIKL_EVICT_MAX_CACHES}")
+    pr, tn = slikl_evict_problem(), slikl_evict_tensors()
+    pr.n_caches, pr.budget, pr.sinks, pr.recent = len(caches), budget, sinks, recent
+    if bsnd:
+        pr.B, pr.S2 = rows
+    else:
+        pr.layout_k, pr.B, pr.S2, pr.T2 = SLIKL_TND, cu_seqlens_k.numel() - 1, int(key_range_bound), rows[0]
+        tn.cu_seqlens_k = _at(cu_seqlens_k, "cu_seqlens_k", index, i32)
+    B = pr.B
+    places = (B, budget)
+    tn.scores = _at(scores, "scores", index, f32)
+    if seq_used_k is not None:
+        tn.seq_used_k = _at(seq_used_k, "seq_used_k", index, i32, (B,))
+    if status is not None:
+        tn.status = _at(status, "status", index, i32, (1,))
+    kept = lengths = new = outs = None
+    if out:
+        kept, lengths, new, outs = out.get("kept"), out.get("lengths"), out.get("scores"), out.get("caches")
+    kept = torch.empty(places, dtype=i32, device=index) if kept is None else kept
+    lengths = torch.empty(B, dtype=i32, device=index) if lengths is None else lengths
+    new = torch.empty(places, dtype=f32, device=index) if new is None else new
+    if outs is None:
+        outs = [torch.zeros(places + c.shape[lead:], dtype=c.dtype, device=index) for c in caches]
+    if len(outs) != len(caches):
+        raise ValueError("out['caches'] must have a tensor for each cache")
+    tn.kept = _at(kept, "kept", index, i32, places)
+    tn.lengths = _at(lengths, "lengths", index, i32, (B,))
+    tn.scores_out = _at(new, "scores (out)", index, f32, places)
+    for i, (c, o) in enumerate(zip(caches, outs)):
+        shape = c.shape
+        if shape[:lead] != rows:
+            raise ValueError(f"cache {i} must have scores' rows")
+        rest = shape[lead:]
+        tn.caches[i] = (_at(c, f"cache {i}", index, c.dtype),
+                        _at(o, f"out cache {i}", index, c.dtype, places + rest),
+                        rest.numel() * c.element_size())
+    _launch(index, slikl_evict, pr, tn)
+    return dict(kept=kept, lengths=lengths, scores=new, caches=outs)

@@ -5,10 +5,20 @@
 // Both kernels are bound by HBM: an element costs 2 + 2 bytes (1 more each way for a checkpoint)
 // against some twenty instructions. A head row of D values is held by D/16 threads, 16 values each,
 // as two 8-value chunks that the rotation by halves pairs with each other: thread l of the first
-// rot_dim/16 takes chunks l and l + rot_dim/16, the others two neighbouring chunks behind the
-// rotated dims. So every load and store is 16 bytes a thread (8 for e4m3), the rotation needs no
-// exchange between threads, and the norm's sums cross at most 8 lanes by shuffles. Statistics,
-// products and sums are fp32; y and dx are rounded once.
+// rot_dim/16 takes chunks l and l + rot_dim/16, the others pair the two halves of the dims behind
+// the rotated ones alike. So every load and store is 16 bytes a thread (8 for e4m3) and neighbours
+// share its 32-byte sectors (two neighbouring chunks a thread, which split each sector over two
+// instructions, took 36 us to copy 134 MB where this takes 22), the rotation needs no exchange
+// between threads, and the norm's sums cross at most 8 lanes by shuffles. Statistics, products and
+// sums are fp32; y and dx are rounded once.
+//
+// HBM wants some 40 KB in flight on each multiprocessor. Registers cannot hold that beside the
+// row being worked on (two blocks of 256 threads with two rows a thread reached half the copy
+// rate), so each thread copies its chunks of the rows to come into a ring in shared memory that
+// it alone reads back: asynchronous copies, several rows deep, and no barrier at all. Next to that
+// the issue slots count (a row of 16 values a thread took 420 instructions in the gradient, which
+// kept it at half the copy rate): arithmetic runs on pairs of fp32 values, and addresses are
+// stepped along the warp's rows instead of computed.
 #include <cuda_fp8.h>
 #include <float.h>
 
@@ -44,7 +54,7 @@ struct Side {
     uint32_t rows;            // head rows T * N
     FastDiv N, S;
     int norm;
-    int64_t x_stride, dx_stride;
+    uint32_t x_stride, dx_stride;   // bytes from one row to the next
     const void *x;
     const uint8_t *x8;
     const float *x8_scale;
@@ -69,8 +79,8 @@ struct Args {
     float *partial;           // gradient: [4][blocks][D] sums of dgain, dbias of q, dgain, dbias of k
 };
 
-constexpr int kThreads = 256;
-constexpr int kGradBlocks = 592;      // most blocks of the gradient kernel (the workspace's size)
+constexpr int kThreads = 128;
+constexpr int kGradBlocks = 1024;     // most blocks of the gradient kernel (the workspace's size)
 
 // What one thread of a head row is responsible for.
 struct Lane {
@@ -80,101 +90,117 @@ struct Lane {
     bool turns;               // rotated dims
 };
 
-__device__ __forceinline__ Lane lane_of(int l, int rot, int pairs) {
+__device__ __forceinline__ Lane lane_of(int l, int rot, int pairs, int D) {
     Lane t;
     const int half = rot / 16;
     t.turns = l < half;
-    t.ca = t.turns ? 8 * l : rot + 16 * (l - half);
-    t.cb = t.turns ? t.ca + rot / 2 : t.ca + 8;
+    t.ca = t.turns ? 8 * l : rot + 8 * (l - half);
+    t.cb = t.ca + (t.turns ? rot : D - rot) / 2;
     t.ta = pairs ? 4 * l : 8 * l;
     t.tb = pairs ? 4 * l + rot / 4 : t.ta + 4;
     return t;
 }
 
-// Position of head row r's token; false for padding and (flagged) for a bad position.
-__device__ __forceinline__ bool position_of(const Args &a, const Side &s, uint32_t token,
-                                            uint32_t &pos) {
-    if (s.positions) {
-        const int32_t p = s.positions[token];
-        pos = (uint32_t)p;
-        if (p < 0 || (a.rot && pos >= a.table_rows)) {
-            if (p != -1 && a.status) set_status(a.status, SLIKL_DEV_BAD_POSITION);
-            return false;
-        }
-        return true;
-    }
-    pos = token - div_by(token, s.S) * s.S.d;
-    if (a.rot && pos >= a.table_rows) {
-        if (a.status) set_status(a.status, SLIKL_DEV_BAD_POSITION);
-        return false;
-    }
-    return true;
+// Two fp32 values and what one instruction does to both.
+union Pair {
+    unsigned long long w;
+    float2 f;
+};
+__device__ __forceinline__ Pair pair(float x, float y) {
+    Pair p;
+    p.f = make_float2(x, y);
+    return p;
 }
+__device__ __forceinline__ Pair operator*(Pair a, Pair b) {
+    Pair d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.w) : "l"(a.w), "l"(b.w));
+    return d;
+}
+__device__ __forceinline__ Pair operator+(Pair a, Pair b) {
+    Pair d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.w) : "l"(a.w), "l"(b.w));
+    return d;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+    Pair d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.w) : "l"(a.w), "l"(b.w), "l"(c.w));
+    return d;
+}
+__device__ __forceinline__ float both(Pair a) { return a.f.x + a.f.y; }
 
-__device__ __forceinline__ void load_angles(const Args &a, const Lane &t, uint32_t pos, float *c,
-                                            float *s) {
-    if (!t.turns) return;
+// The thread's 16 values as pairs of neighbours: [0, 4) its first chunk, [4, 8) its second.
+// c, s: cosines and sines of its 8 angles.
+struct Angles {
+    Pair c[4], s[4];
+};
+
+__device__ __forceinline__ void load_angles(const Args &a, const Lane &t, int32_t pos, Angles &g) {
     const float *row = a.cos_sin + (int64_t)pos * a.rot;
-    const float4 c0 = *reinterpret_cast<const float4 *>(row + t.ta);
-    const float4 c1 = *reinterpret_cast<const float4 *>(row + t.tb);
-    const float4 s0 = *reinterpret_cast<const float4 *>(row + a.rot / 2 + t.ta);
-    const float4 s1 = *reinterpret_cast<const float4 *>(row + a.rot / 2 + t.tb);
-    c[0] = c0.x; c[1] = c0.y; c[2] = c0.z; c[3] = c0.w;
-    c[4] = c1.x; c[5] = c1.y; c[6] = c1.z; c[7] = c1.w;
-    s[0] = s0.x; s[1] = s0.y; s[2] = s0.z; s[3] = s0.w;
-    s[4] = s1.x; s[5] = s1.y; s[6] = s1.z; s[7] = s1.w;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const float4 c = *reinterpret_cast<const float4 *>(row + (h ? t.tb : t.ta));
+        const float4 s = *reinterpret_cast<const float4 *>(row + a.rot / 2 + (h ? t.tb : t.ta));
+        g.c[2 * h] = pair(c.x, c.y), g.c[2 * h + 1] = pair(c.z, c.w);
+        g.s[2 * h] = pair(s.x, s.y), g.s[2 * h + 1] = pair(s.z, s.w);
+    }
 }
 
-// v[0..8) is the thread's first chunk, v[8..16) its second; sign -1 turns back.
-__device__ __forceinline__ void turn(float *v, const float *c, const float *s, int pairs,
-                                     float sign) {
+// Turns the values by the angles, or (BACK) by minus the angles. Halves: pairs of angles meet pairs
+// of values. Pairs: the angle of v[i] is half i & 1 of angle pair i / 2.
+template <bool BACK>
+__device__ __forceinline__ void turn(Pair *v, const Angles &g, int pairs) {
     if (pairs) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float x = v[2 * i], y = v[2 * i + 1], sn = sign * s[i];
-            v[2 * i] = x * c[i] - y * sn;
-            v[2 * i + 1] = y * c[i] + x * sn;
+            const float c = i & 1 ? g.c[i / 2].f.y : g.c[i / 2].f.x;
+            const float s0 = i & 1 ? g.s[i / 2].f.y : g.s[i / 2].f.x, s = BACK ? -s0 : s0;
+            const float x = v[i].f.x, y = v[i].f.y;
+            v[i].f.x = fmaf(x, c, -(y * s));
+            v[i].f.y = fmaf(y, c, x * s);
         }
     } else {
+        const Pair minus = pair(-1.f, -1.f);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float x = v[i], y = v[i + 8], sn = sign * s[i];
-            v[i] = x * c[i] - y * sn;
-            v[i + 8] = y * c[i] + x * sn;
+        for (int i = 0; i < 4; ++i) {
+            const Pair x = v[i], y = v[i + 4], xs = x * g.s[i], ys = y * g.s[i];
+            v[i] = fma2(x, g.c[i], BACK ? ys : ys * minus);
+            v[i + 4] = fma2(y, g.c[i], BACK ? xs * minus : xs);
         }
     }
 }
 
 template <typename T>
-__device__ __forceinline__ void widen(const uint4 &a, const uint4 &b, float *v) {
+__device__ __forceinline__ void widen(const uint4 &a, const uint4 &b, Pair *v) {
     const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float2 f = unpack2<T>(w[i]);
-        v[2 * i] = f.x;
-        v[2 * i + 1] = f.y;
-    }
+    for (int i = 0; i < 8; ++i) v[i].f = unpack2<T>(w[i]);
 }
 
-__device__ __forceinline__ void widen8(const uint2 &a, const uint2 &b, float scale, float *v) {
+__device__ __forceinline__ void widen8(const uint2 &a, const uint2 &b, float scale, Pair *v) {
     const uint32_t w[4] = {a.x, a.y, b.x, b.y};
+    const Pair s = pair(scale, scale);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const __nv_fp8x2_storage_t two = (__nv_fp8x2_storage_t)(w[i >> 1] >> (16 * (i & 1)));
         const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(two, __NV_E4M3);
-        const float2 f = __half22float2(__half2(h));
-        v[2 * i] = f.x * scale;
-        v[2 * i + 1] = f.y * scale;
+        v[i].f = __half22float2(__half2(h));
+        v[i] = v[i] * s;
     }
 }
 
+// Stores the thread's 16 values as 16-bit ones; `first`: where its first chunk goes.
 template <typename T>
-__device__ __forceinline__ void narrow_store(T *row, const Lane &t, const float *v) {
+__device__ __forceinline__ void narrow_store(char *first, const Lane &t, const Pair *v) {
     uint32_t w[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = pack2<T>(v[2 * i], v[2 * i + 1]);
-    *reinterpret_cast<uint4 *>(row + t.ca) = make_uint4(w[0], w[1], w[2], w[3]);
-    *reinterpret_cast<uint4 *>(row + t.cb) = make_uint4(w[4], w[5], w[6], w[7]);
+    for (int i = 0; i < 8; ++i) w[i] = pack2<T>(v[i].f.x, v[i].f.y);
+    *reinterpret_cast<uint4 *>(first) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4 *>(first + 2 * (t.cb - t.ca)) = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
+__device__ __forceinline__ void zero_store(char *first, const Lane &t) {
+    *reinterpret_cast<uint4 *>(first) = make_uint4(0, 0, 0, 0);
+    *reinterpret_cast<uint4 *>(first + 2 * (t.cb - t.ca)) = make_uint4(0, 0, 0, 0);
 }
 
 // Sum (or maximum) over the threads of a head row; every one gets the same bits.
@@ -191,242 +217,394 @@ __device__ __forceinline__ float row_max(float v) {
     return v;
 }
 
-// x -> (x - m) r in place; returns r. The variance is taken about the mean, not as a difference
-// of moments, so that a mean far above the deviation costs no digits.
+// Takes the row's mean off x (layer norm) and returns r. The variance is taken about the mean, not
+// as a difference of moments, so that a mean far above the deviation costs no digits.
 template <int D, int NORM>
-__device__ __forceinline__ float normalise(float *x, float eps) {
-    if (NORM == SLIKL_NORM_NONE) return 1.f;
+__device__ __forceinline__ float centre(Pair *x, float eps) {
     constexpr int TPR = D / 16;
     if (NORM == SLIKL_NORM_LAYER) {
-        float m = 0.f;
+        Pair m = x[0];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) m += x[i];
-        m = row_sum<TPR>(m) * (1.f / D);
+        for (int i = 1; i < 8; ++i) m = m + x[i];
+        const float mean = row_sum<TPR>(both(m)) * (-1.f / D);
+        const Pair less = pair(mean, mean);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] -= m;
+        for (int i = 0; i < 8; ++i) x[i] = x[i] + less;
     }
-    float q = 0.f;
+    Pair q = x[0] * x[0];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) q = fmaf(x[i], x[i], q);
-    const float r = rsqrtf(fmaf(row_sum<TPR>(q), 1.f / D, eps));
-#pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] *= r;
-    return r;
+    for (int i = 1; i < 8; ++i) q = fma2(x[i], x[i], q);
+    return rsqrtf(fmaf(row_sum<TPR>(both(q)), 1.f / D, eps));
 }
 
-// The row of x (or of its checkpoint) as the thread's 16 values.
-template <typename T, int D, bool SRC8>
-struct Raw {
-    uint4 a, b;
-    uint2 a8, b8;
-    float scale;
-    __device__ __forceinline__ void load(const Side &s, uint32_t row, uint32_t token,
-                                         const Lane &t) {
-        if (SRC8) {
-            const uint8_t *p = s.x8 + (int64_t)row * D;
-            a8 = *reinterpret_cast<const uint2 *>(p + t.ca);
-            b8 = *reinterpret_cast<const uint2 *>(p + t.cb);
-            scale = s.x8_scale[row];
-        } else {
-            const T *p = static_cast<const T *>(s.x) + (int64_t)token * s.x_stride +
-                         (row - token * s.N.d) * D;
-            a = *reinterpret_cast<const uint4 *>(p + t.ca);
-            b = *reinterpret_cast<const uint4 *>(p + t.cb);
-        }
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+
+// A stage of the threads' rings: a row of x (two 16-byte chunks, or two 8-byte ones and the scale of
+// a checkpoint), of dy (two 16-byte chunks) and its position. Neighbouring threads' chunks are
+// neighbours, so no access has a bank conflict.
+template <bool SRC8, bool GRAD>
+struct Stage {
+    uint4 x[SRC8 ? 1 : 2][kThreads];       // (a checkpoint's two 8-byte chunks are x[0][i])
+    uint4 dy[GRAD ? 2 : 1][GRAD ? kThreads : 1];
+    float scale[SRC8 ? kThreads : 1];
+    int32_t pos[kThreads];                 // -1: the row takes no part
+};
+constexpr int kStages = 4;
+template <bool SRC8, bool GRAD>
+using Ring = Stage<SRC8, GRAD>[kStages];
+
+// The rows of a warp: groups of RPW = 512 / D rows next to one another, an equal share of the
+// side's groups. `row` is the thread's row in the group, which it steps through together with its
+// token and head; rows behind the side's last one are worked on like the others, but neither read
+// nor stored.
+template <int RPW>
+struct Walk {
+    uint32_t row, token, head;
+    int32_t steps;
+    uint32_t dt, dh;          // a step of RPW rows is dt tokens and dh heads
+    __device__ __forceinline__ Walk(const Side &s, uint32_t block, uint32_t blocks, int sub) {
+        const uint32_t groups = (s.rows + RPW - 1) / RPW;
+        const uint32_t warp = block * (kThreads / 32) + (threadIdx.x >> 5);
+        const uint32_t warps = blocks * (kThreads / 32);
+        const uint32_t begin = (uint32_t)((uint64_t)groups * warp / warps);
+        steps = (int32_t)((uint32_t)((uint64_t)groups * (warp + 1) / warps) - begin);
+        row = begin * RPW + sub;
+        token = div_by(row, s.N);
+        head = row - token * s.N.d;
+        dt = div_by(RPW, s.N);
+        dh = RPW - dt * s.N.d;
     }
-    __device__ __forceinline__ void values(float *v) const {
-        if (SRC8) widen8(a8, b8, scale, v);
-        else widen<T>(a, b, v);
+    __device__ __forceinline__ void step(const Side &s) {
+        row += RPW;
+        token += dt;
+        head += dh;
+        if (head >= s.N.d) {
+            head -= s.N.d;
+            ++token;
+        }
     }
 };
 
-__device__ __forceinline__ void load16(const float *p, const Lane &t, float *v) {
+// Copies the rows to come into the ring.
+template <typename T, int D, bool SRC8, bool GRAD, bool READS_X>
+struct Fetch {
+    Walk<512 / D> w;
+    const char *x, *dy;       // the thread's first chunk of row 0
+    int32_t pos, last;        // the walk's position, read a step early, and the one before
+    uint32_t stage;
+
+    __device__ __forceinline__ Fetch(const Args &a, const Side &s, const Lane &t,
+                                     const Walk<512 / D> &from)
+        : w(from), last(-1), stage(0) {
+        x = SRC8 ? reinterpret_cast<const char *>(s.x8) + t.ca
+                 : static_cast<const char *>(s.x) + 2 * t.ca;
+        dy = static_cast<const char *>(s.dy) + 2 * t.ca;
+        find_position(a, s);
+    }
+    // The row's position, -1 where it takes no part; a bad one is flagged.
+    __device__ __forceinline__ void find_position(const Args &a, const Side &s) {
+        pos = -1;
+        if (w.row >= s.rows) return;
+        pos = s.positions ? s.positions[w.token]
+                          : (int32_t)(w.token - div_by(w.token, s.S) * s.S.d);
+    }
+    // Starts the copies of the walk's row, brings its angles near, and steps on. (A row's angles are
+    // loaded when it is worked on, often once for many heads; keys of one head need new ones each
+    // row, and without the prefetch their side took twice as long as the queries'.)
+    __device__ __forceinline__ void next(Ring<SRC8, GRAD> &ring, const Args &a, const Side &s,
+                                         const Lane &t) {
+        Stage<SRC8, GRAD> &to = ring[stage];
+        stage = (stage + 1) % kStages;
+        const int i = threadIdx.x;
+        if (pos < 0 || (a.rot && (uint32_t)pos >= a.table_rows)) {
+            if (pos != -1 && a.status) set_status(a.status, SLIKL_DEV_BAD_POSITION);
+            pos = -1;
+        } else if (t.turns && pos != last) {
+            const float *row = a.cos_sin + (int64_t)pos * a.rot + t.ta;
+            asm volatile("prefetch.global.L1 [%0];" ::"l"(row));
+            asm volatile("prefetch.global.L1 [%0];" ::"l"(row + a.rot / 2));
+        }
+        to.pos[i] = last = pos;
+        if (w.row < s.rows) {
+            if (READS_X && SRC8) {
+                const char *p = x + (uint64_t)w.row * D;
+                const uint32_t at = sm100::smem_u32(&to.x[0][i]);
+                cp_async8(at, p);
+                cp_async8(at + 8, p + (t.cb - t.ca));
+                cp_async4(sm100::smem_u32(&to.scale[i]), s.x8_scale + w.row);
+            } else if (READS_X) {
+                const char *p = x + (uint64_t)w.token * s.x_stride + w.head * (2 * D);
+                sm100::cp_async16(sm100::smem_u32(&to.x[0][i]), p, 16);
+                sm100::cp_async16(sm100::smem_u32(&to.x[SRC8 ? 0 : 1][i]), p + 2 * (t.cb - t.ca), 16);
+            }
+            if (GRAD) {
+                const char *p = dy + (uint64_t)w.row * (2 * D);
+                sm100::cp_async16(sm100::smem_u32(&to.dy[0][i]), p, 16);
+                sm100::cp_async16(sm100::smem_u32(&to.dy[GRAD ? 1 : 0][i]), p + 2 * (t.cb - t.ca), 16);
+            }
+        }
+        cp_async_commit();
+        w.step(s);
+        find_position(a, s);
+    }
+};
+
+template <typename T, bool SRC8, bool GRAD>
+__device__ __forceinline__ void source(const Stage<SRC8, GRAD> &from, Pair *v) {
+    const int i = threadIdx.x;
+    const uint4 x = from.x[0][i];
+    if (SRC8) widen8(make_uint2(x.x, x.y), make_uint2(x.z, x.w), from.scale[SRC8 ? i : 0], v);
+    else widen<T>(x, from.x[SRC8 ? 0 : 1][i], v);
+}
+
+__device__ __forceinline__ void load16(const float *p, const Lane &t, Pair *v) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const float4 *q = reinterpret_cast<const float4 *>(p + (h ? t.cb : t.ca));
         const float4 u = q[0], w = q[1];
-        v[8 * h] = u.x; v[8 * h + 1] = u.y; v[8 * h + 2] = u.z; v[8 * h + 3] = u.w;
-        v[8 * h + 4] = w.x; v[8 * h + 5] = w.y; v[8 * h + 6] = w.z; v[8 * h + 7] = w.w;
+        v[4 * h] = pair(u.x, u.y), v[4 * h + 1] = pair(u.z, u.w);
+        v[4 * h + 2] = pair(w.x, w.y), v[4 * h + 3] = pair(w.z, w.w);
     }
 }
 
-// One e4m3 checkpoint row: scale = max|x| / 448, values x / scale (a product with the scale's
-// reciprocal, which may round a value halfway between two codes the other way). Every lane of the
-// warp has to come here (the maximum crosses lanes); rows that are not `in` are not stored.
-template <int D>
-__device__ __forceinline__ void keep_row(const Side &s, uint32_t row, const Lane &t, int l,
-                                         bool in, bool live, const float *x) {
-    float top = 0.f;
+// Largest magnitude of a chunk's eight 16-bit values, NaN aside, in both halves of the word.
+template <typename T>
+__device__ __forceinline__ uint32_t top_of(const uint4 &a, const uint4 &b);
+template <>
+__device__ __forceinline__ uint32_t top_of<__nv_bfloat16>(const uint4 &a, const uint4 &b) {
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    __nv_bfloat162 m = __habs2(reinterpret_cast<const __nv_bfloat162 &>(w[0]));
 #pragma unroll
-    for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(x[i]));
-    top = row_max<D / 16>(top);
+    for (int i = 1; i < 8; ++i) m = __hmax2(m, __habs2(reinterpret_cast<const __nv_bfloat162 &>(w[i])));
+    return reinterpret_cast<const uint32_t &>(m);
+}
+template <>
+__device__ __forceinline__ uint32_t top_of<__half>(const uint4 &a, const uint4 &b) {
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    __half2 m = __habs2(reinterpret_cast<const __half2 &>(w[0]));
+#pragma unroll
+    for (int i = 1; i < 8; ++i) m = __hmax2(m, __habs2(reinterpret_cast<const __half2 &>(w[i])));
+    return reinterpret_cast<const uint32_t &>(m);
+}
+
+// One e4m3 checkpoint row: scale = max|x| / 448, values x / scale. Both divisions are products with
+// reciprocals: the scale may be off by its last bit, and a value halfway between two codes may
+// round the other way. Every lane of the warp has to come here (the maximum crosses lanes); rows
+// that are not `in` are not stored. `top`: top_of the thread's values.
+template <typename T, int D>
+__device__ __forceinline__ void keep_row(const Side &s, uint32_t row, const Lane &t, int l,
+                                         bool in, bool live, uint32_t top, const Pair *x) {
+    const float2 two = unpack2<T>(top);
+    const float m = row_max<D / 16>(fmaxf(two.x, two.y));
     if (!in) return;
     // a row of subnormal bf16 values keeps a normal scale, so that its reciprocal is finite
-    const float scale = live && top > 0.f ? fmaxf(top / 448.f, FLT_MIN) : 0.f;
-    const float inv = scale > 0.f ? 1.f / scale : 0.f;
+    const bool some = live && m > 0.f;
+    const float scale = some ? fmaxf(m * (1.f / 448.f), FLT_MIN) : 0.f;
+    const float inv = some ? __fdividef(1.f, scale) : 0.f;
     uint32_t w[4] = {0, 0, 0, 0};
     if (live) {
+        const Pair by = pair(inv, inv);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t two = __nv_cvt_float2_to_fp8x2(
-                make_float2(x[2 * i] * inv, x[2 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
-            w[i >> 1] |= two << (16 * (i & 1));
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t lo = __nv_cvt_float2_to_fp8x2((x[2 * i] * by).f, __NV_SATFINITE, __NV_E4M3);
+            const uint32_t hi = __nv_cvt_float2_to_fp8x2((x[2 * i + 1] * by).f, __NV_SATFINITE, __NV_E4M3);
+            w[i] = __byte_perm(lo, hi, 0x5410);
         }
     }
-    uint8_t *p = s.keep8 + (int64_t)row * D;
-    *reinterpret_cast<uint2 *>(p + t.ca) = make_uint2(w[0], w[1]);
-    *reinterpret_cast<uint2 *>(p + t.cb) = make_uint2(w[2], w[3]);
+    uint8_t *p = s.keep8 + t.ca + (uint64_t)row * D;
+    *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+    *reinterpret_cast<uint2 *>(p + (t.cb - t.ca)) = make_uint2(w[2], w[3]);
     if (l == 0) s.keep8_scale[row] = scale;
 }
 
-// Forward: each warp takes kFwdUnroll * 512 / D consecutive head rows, all of them loaded before
-// the first is worked on.
-constexpr int kFwdUnroll = 2;
-
 template <typename T, int D, int NORM, bool SRC8>
-__device__ __forceinline__ void forward_rows(const Args &a, const Side &s, uint32_t block) {
+__device__ __forceinline__ void forward_rows(const Args &a, const Side &s, uint32_t block,
+                                             uint32_t blocks, void *smem) {
     constexpr int TPR = D / 16, RPW = 32 / TPR;
-    const int lane = threadIdx.x & 31, l = lane % TPR;
-    const Lane t = lane_of(l, a.rot, a.pairs);
-    const uint32_t first = (block * (kThreads / 32) + (threadIdx.x >> 5)) * (RPW * kFwdUnroll) +
-                           lane / TPR;
-    Raw<T, D, SRC8> raw[kFwdUnroll];
-    uint32_t token[kFwdUnroll];
+    auto &ring = *static_cast<Ring<SRC8, false> *>(smem);
+    const int l = (threadIdx.x & 31) % TPR;
+    const Lane t = lane_of(l, a.rot, a.pairs, D);
+    const Walk<RPW> walk(s, block, blocks, (threadIdx.x & 31) / TPR);
+    const int32_t steps = walk.steps;
+    uint32_t row = walk.row, stage = 0;
+    Fetch<T, D, SRC8, false, true> fetch(a, s, t, walk);
 #pragma unroll
-    for (int u = 0; u < kFwdUnroll; ++u) {
-        // rows behind the last one are worked on as copies of it and not stored
-        const uint32_t row = min(first + u * RPW, s.rows - 1);
-        token[u] = div_by(row, s.N);
-        raw[u].load(s, row, token[u], t);
+    for (int i = 0; i < kStages - 1; ++i) {
+        if (i < steps) fetch.next(ring, a, s, t);
+        else cp_async_commit();
     }
-    float gain[16], bias[16];
+    Pair gain[8];
+    Angles angles;
+    int32_t turned_to = -1;               // the position that `angles` belongs to
     if (NORM != SLIKL_NORM_NONE && s.gain) load16(s.gain, t, gain);
-    if (NORM == SLIKL_NORM_LAYER && s.bias) load16(s.bias, t, bias);
-#pragma unroll
-    for (int u = 0; u < kFwdUnroll; ++u) {
-        const uint32_t row = first + u * RPW;
-        const bool in = row < s.rows;
-        uint32_t pos = 0;
-        const bool live = position_of(a, s, token[u], pos);
-        float v[16];
-        raw[u].values(v);
-        if (!SRC8 && s.keep8) keep_row<D>(s, row, t, l, in, live, v);
+    for (int32_t i = 0; i < steps; ++i, row += RPW) {
+        sm100::cp_async_wait<kStages - 2>();
+        const Stage<SRC8, false> &now = ring[stage];
+        stage = (stage + 1) % kStages;
+        const int32_t pos = now.pos[threadIdx.x];
+        const bool in = row < s.rows, live = pos >= 0;
+        if (live && t.turns && pos != turned_to) {
+            load_angles(a, t, pos, angles);
+            turned_to = pos;
+        }
+        Pair v[8];
+        source<T>(now, v);
+        uint32_t top = 0;
+        if (!SRC8 && s.keep8) top = top_of<T>(now.x[0][threadIdx.x], now.x[SRC8 ? 0 : 1][threadIdx.x]);
+        if (i + kStages - 1 < steps) fetch.next(ring, a, s, t);
+        else cp_async_commit();
+        if (!SRC8 && s.keep8) keep_row<T, D>(s, row, t, l, in, live, top, v);
         if (!s.y) continue;
-        normalise<D, NORM>(v, a.eps);
-        if (NORM != SLIKL_NORM_NONE && s.gain) {
+        if (NORM != SLIKL_NORM_NONE) {
+            const float r = centre<D, NORM>(v, a.eps);
+            const Pair by = pair(r, r);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] *= gain[i];
+            for (int j = 0; j < 8; ++j) v[j] = v[j] * by;
+            if (s.gain) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = v[j] * gain[j];
+            }
         }
         if (NORM == SLIKL_NORM_LAYER && s.bias) {
+            Pair bias[8];
+            load16(s.bias, t, bias);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] += bias[i];
+            for (int j = 0; j < 8; ++j) v[j] = v[j] + bias[j];
         }
         if (!in) continue;
+        char *y = static_cast<char *>(s.y) + 2 * t.ca + (uint64_t)row * (2 * D);
         if (!live) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = 0.f;
-        } else if (t.turns) {
-            float c[8], sn[8];
-            load_angles(a, t, pos, c, sn);
-            turn(v, c, sn, a.pairs, 1.f);
+            zero_store(y, t);
+            continue;
         }
-        narrow_store<T>(static_cast<T *>(s.y) + (int64_t)row * D, t, v);
+        if (t.turns) turn<false>(v, angles, a.pairs);
+        narrow_store<T>(y, t, v);
     }
 }
 
 template <typename T, int D, bool SRC8>
-__device__ __forceinline__ void forward_side(const Args &a, const Side &s, uint32_t block) {
-    if (s.norm == SLIKL_NORM_RMS) forward_rows<T, D, SLIKL_NORM_RMS, SRC8>(a, s, block);
-    else if (s.norm == SLIKL_NORM_LAYER) forward_rows<T, D, SLIKL_NORM_LAYER, SRC8>(a, s, block);
-    else forward_rows<T, D, SLIKL_NORM_NONE, SRC8>(a, s, block);
+__device__ __forceinline__ void forward_side(const Args &a, const Side &s, uint32_t block,
+                                             uint32_t blocks, void *smem) {
+    if (s.norm == SLIKL_NORM_RMS)
+        forward_rows<T, D, SLIKL_NORM_RMS, SRC8>(a, s, block, blocks, smem);
+    else if (s.norm == SLIKL_NORM_LAYER)
+        forward_rows<T, D, SLIKL_NORM_LAYER, SRC8>(a, s, block, blocks, smem);
+    else
+        forward_rows<T, D, SLIKL_NORM_NONE, SRC8>(a, s, block, blocks, smem);
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) qk_forward(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kThreads, 5) qk_forward(const __grid_constant__ Args a) {
+    __shared__ __align__(16) unsigned char smem[sizeof(Ring<false, false>)];
+    static_assert(sizeof(Ring<true, false>) <= sizeof(smem), "ring of a checkpoint");
     const bool k = blockIdx.x >= a.blocks_q;
     const Side &s = a.side[k];
-    const uint32_t block = blockIdx.x - (k ? a.blocks_q : 0);
-    if (s.x) forward_side<T, D, false>(a, s, block);
-    else forward_side<T, D, true>(a, s, block);
+    const uint32_t block = blockIdx.x - (k ? a.blocks_q : 0), blocks = k ? a.blocks_k : a.blocks_q;
+    if (s.x) forward_side<T, D, false>(a, s, block, blocks, smem);
+    else forward_side<T, D, true>(a, s, block, blocks, smem);
 }
 
-// Gradient: a block takes a contiguous share of the side's rows, its warps side by side, with the
-// next rows' loads in flight while the present ones are worked on. The sums of dgain and dbias
-// stay in registers over the whole share, are added over the block in a fixed order and stored;
-// qk_grad_sums adds the blocks' sums, again in a fixed order.
+// Gradient: the sums of dgain and dbias stay in registers over a warp's rows, are added over the
+// block in a fixed order and stored; qk_grad_sums adds the blocks' sums, again in a fixed order.
+// With x less its mean, e = dz r and u = e gain:
+//   dgain += e x,  dbias += dz,  dx = u - x r^2 mean(u x) - mean(u)      (the last for layer only)
 template <typename T, int D, int NORM, bool SRC8>
 __device__ __forceinline__ void gradient_rows(const Args &a, const Side &s, uint32_t block,
-                                              uint32_t blocks, float *partial, float *smem) {
-    constexpr int TPR = D / 16, RPW = 32 / TPR, WARPS = kThreads / 32, TILE = WARPS * RPW;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % TPR;
-    const Lane t = lane_of(l, a.rot, a.pairs);
-    const uint32_t tiles = (s.rows + TILE - 1) / TILE;
-    const uint32_t begin = (uint32_t)((uint64_t)tiles * block / blocks);
-    const uint32_t end = (uint32_t)((uint64_t)tiles * (block + 1) / blocks);
-    float gain[16], dgain[16], dbias[16];
+                                              uint32_t blocks, float *partial, void *ring_smem) {
+    constexpr int TPR = D / 16, RPW = 32 / TPR, WARPS = kThreads / 32;
+    constexpr bool X = NORM != SLIKL_NORM_NONE;        // without a norm x is not needed
+    auto &ring = *static_cast<Ring<SRC8, true> *>(ring_smem);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const Lane t = lane_of(lane % TPR, a.rot, a.pairs, D);
+    Walk<RPW> at(s, block, blocks, lane / TPR);
+    const int32_t steps = at.steps;
+    uint32_t stage = 0;
+    Fetch<T, D, SRC8, true, X> fetch(a, s, t, at);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) gain[i] = 1.f, dgain[i] = 0.f, dbias[i] = 0.f;
-    if (NORM != SLIKL_NORM_NONE && s.gain) load16(s.gain, t, gain);
-
-    Raw<T, D, SRC8> x, x_next;
-    uint4 ga, gb, ga_next, gb_next;
-    uint32_t token = 0, token_next = 0;
-    auto fetch = [&](uint32_t tile) {
-        const uint32_t row = min(tile * TILE + warp * RPW + lane / TPR, s.rows - 1);
-        token_next = div_by(row, s.N);
-        if (NORM != SLIKL_NORM_NONE) x_next.load(s, row, token_next, t);
-        const T *g = static_cast<const T *>(s.dy) + (int64_t)row * D;
-        ga_next = *reinterpret_cast<const uint4 *>(g + t.ca);
-        gb_next = *reinterpret_cast<const uint4 *>(g + t.cb);
-    };
-    if (begin < end) fetch(begin);
-    for (uint32_t tile = begin; tile < end; ++tile) {
-        x = x_next, ga = ga_next, gb = gb_next, token = token_next;
-        const uint32_t row = tile * TILE + warp * RPW + lane / TPR;
-        const bool in = row < s.rows;
-        uint32_t pos = 0;
-        const bool live = position_of(a, s, token, pos);
-        float g[16];
-        widen<T>(ga, gb, g);
-        if (live && t.turns) {
-            float c[8], sn[8];
-            load_angles(a, t, pos, c, sn);
-            turn(g, c, sn, a.pairs, -1.f);
+    for (int i = 0; i < kStages - 1; ++i) {
+        if (i < steps) fetch.next(ring, a, s, t);
+        else cp_async_commit();
+    }
+    Pair gain[8], dgain[8], dbias[8];
+    Angles angles;
+    int32_t turned_to = -1;
+    if (X) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) gain[i] = pair(1.f, 1.f), dgain[i] = dbias[i] = pair(0.f, 0.f);
+        if (s.gain) load16(s.gain, t, gain);
+    }
+    for (int32_t i = 0; i < steps; ++i, at.step(s)) {
+        sm100::cp_async_wait<kStages - 2>();
+        const Stage<SRC8, true> &now = ring[stage];
+        stage = (stage + 1) % kStages;
+        const int32_t pos = now.pos[threadIdx.x];
+        const bool in = at.row < s.rows, live = pos >= 0;
+        if (live && t.turns && pos != turned_to) {
+            load_angles(a, t, pos, angles);
+            turned_to = pos;
         }
-        if (tile + 1 < end) fetch(tile + 1);
-        if (NORM != SLIKL_NORM_NONE) {
-            float v[16];
-            x.values(v);
-            const float r = normalise<D, NORM>(v, a.eps);
-            const bool counts = in && live;
-            float su = 0.f, sv = 0.f;
+        Pair g[8], v[8];
+        widen<T>(now.dy[0][threadIdx.x], now.dy[1][threadIdx.x], g);
+        if (X) source<T>(now, v);
+        if (i + kStages - 1 < steps) fetch.next(ring, a, s, t);
+        else cp_async_commit();
+        if (live && t.turns) turn<true>(g, angles, a.pairs);
+        if (X) {
+            const float r = centre<D, NORM>(v, a.eps);
+            const Pair by = pair(r, r);
+            if (live) {                   // (rows behind the last one are at position -1)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                if (counts) {
-                    dgain[i] = fmaf(g[i], v[i], dgain[i]);
-                    if (NORM == SLIKL_NORM_LAYER) dbias[i] += g[i];
+                for (int j = 0; j < 8; ++j) {
+                    if (NORM == SLIKL_NORM_LAYER) dbias[j] = dbias[j] + g[j];
+                    g[j] = g[j] * by;
+                    dgain[j] = fma2(g[j], v[j], dgain[j]);
                 }
-                g[i] *= gain[i];
-                su += g[i];
-                sv = fmaf(g[i], v[i], sv);
             }
-            sv = row_sum<TPR>(sv) * (1.f / D);
-            su = NORM == SLIKL_NORM_LAYER ? row_sum<TPR>(su) * (1.f / D) : 0.f;
+            Pair su, sv;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) g[i] = r * (g[i] - su - v[i] * sv);
+            for (int j = 0; j < 8; ++j) {
+                g[j] = g[j] * gain[j];
+                su = j ? su + g[j] : g[j];
+                sv = j ? fma2(g[j], v[j], sv) : g[j] * v[j];
+            }
+            const float m = row_sum<TPR>(both(sv)) * (r * r * (-1.f / D));
+            const Pair along = pair(m, m);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) g[j] = fma2(v[j], along, g[j]);
+            if (NORM == SLIKL_NORM_LAYER) {
+                const float l = row_sum<TPR>(both(su)) * (-1.f / D);
+                const Pair less = pair(l, l);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) g[j] = g[j] + less;
+            }
         }
         if (!in) continue;
-        if (!live) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) g[i] = 0.f;
-        }
-        narrow_store<T>(static_cast<T *>(s.dx) + (int64_t)token * s.dx_stride +
-                            (row - token * s.N.d) * D, t, g);
+        char *dx = static_cast<char *>(s.dx) + 2 * t.ca + (uint64_t)at.token * s.dx_stride +
+                   at.head * (2 * D);
+        if (live) narrow_store<T>(dx, t, g);
+        else zero_store(dx, t);
     }
+    // the ring's memory serves the sum over the block's warps once every warp is done with it
+    sm100::cp_async_wait<0>();
+    __syncthreads();
+    float *smem = static_cast<float *>(ring_smem);
     if constexpr (NORM != SLIKL_NORM_NONE) {
 #pragma unroll
         for (int which = 0; which < (NORM == SLIKL_NORM_LAYER ? 2 : 1); ++which) {
-            float *acc = which ? dbias : dgain;
+            float acc[16];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                acc[2 * i] = which ? dbias[i].f.x : dgain[i].f.x;
+                acc[2 * i + 1] = which ? dbias[i].f.y : dgain[i].f.y;
+            }
 #pragma unroll
             for (int i = 0; i < 16; ++i)
 #pragma unroll
@@ -452,7 +630,7 @@ __device__ __forceinline__ void gradient_rows(const Args &a, const Side &s, uint
 
 template <typename T, int D, bool SRC8>
 __device__ __forceinline__ void gradient_side(const Args &a, const Side &s, uint32_t block,
-                                              uint32_t blocks, float *partial, float *smem) {
+                                              uint32_t blocks, float *partial, void *smem) {
     if (s.norm == SLIKL_NORM_RMS)
         gradient_rows<T, D, SLIKL_NORM_RMS, SRC8>(a, s, block, blocks, partial, smem);
     else if (s.norm == SLIKL_NORM_LAYER)
@@ -462,8 +640,9 @@ __device__ __forceinline__ void gradient_side(const Args &a, const Side &s, uint
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, 2) qk_gradient(const __grid_constant__ Args a) {
-    __shared__ float smem[(kThreads / 32) * D];
+__global__ void __launch_bounds__(kThreads, 4) qk_gradient(const __grid_constant__ Args a) {
+    __shared__ __align__(16) unsigned char smem[sizeof(Ring<false, true>)];
+    static_assert(sizeof(Ring<true, true>) <= sizeof(smem), "ring of a checkpoint");
     const bool k = blockIdx.x >= a.blocks_q;
     const Side &s = a.side[k];
     const uint32_t block = blockIdx.x - (k ? a.blocks_q : 0);
@@ -578,8 +757,8 @@ Side make_side(const slikl_qk_problem *p, const slikl_qk_side &s, const slikl_qk
     d.N = fast_div((uint32_t)s.N);
     d.S = fast_div(s.S >= 1 && s.S < (int64_t(1) << 31) ? (uint32_t)s.S : 0x7fffffffu);
     d.norm = s.norm;
-    d.x_stride = s.x_stride ? s.x_stride : s.N * p->D;
-    d.dx_stride = s.dx_stride ? s.dx_stride : s.N * p->D;
+    d.x_stride = (uint32_t)(2 * (s.x_stride ? s.x_stride : s.N * p->D));
+    d.dx_stride = (uint32_t)(2 * (s.dx_stride ? s.dx_stride : s.N * p->D));
     d.x = t.x;
     d.x8 = static_cast<const uint8_t *>(t.x8);
     d.x8_scale = t.x8_scale;
@@ -614,11 +793,29 @@ bool on_sm100() {
            major == 10;
 }
 
+// Blocks of both sides, `most` at most, in proportion to the bytes they move (`each` for an element,
+// the angles for a token); a side with rows gets one at least. A small call gets a group of rows for
+// each warp, so that it spreads over all multiprocessors.
+void share_blocks(Args &a, int64_t D, uint32_t most, int each) {
+    const uint32_t tile = (uint32_t)(kThreads / 32) * (uint32_t)(512 / D);
+    uint32_t tiles[2];
+    double bytes[2];
+    for (int i = 0; i < 2; ++i) {
+        const Side &s = a.side[i];
+        tiles[i] = (s.rows + tile - 1) / tile;
+        bytes[i] = (double)s.rows * ((double)each * D + 4.0 * a.rot / s.N.d);
+    }
+    a.blocks_q = tiles[0];
+    a.blocks_k = tiles[1];
+    if ((uint64_t)tiles[0] + tiles[1] <= most) return;
+    const uint32_t share = (uint32_t)(most * (bytes[1] / (bytes[0] + bytes[1])) + 0.5);
+    a.blocks_k = tiles[1] == 0 ? 0 : std::min(tiles[1], std::max(share, 1u));
+    a.blocks_q = std::min(tiles[0], most - a.blocks_k);
+}
+
 slikl_status run_forward(const slikl_qk_problem *p, const slikl_qk_tensors *t, cudaStream_t st) {
     Args a = make_args(p, t);
-    const uint32_t per_block = (kThreads / 32) * kFwdUnroll * (uint32_t)(512 / p->D);
-    a.blocks_q = (a.side[0].rows + per_block - 1) / per_block;
-    a.blocks_k = (a.side[1].rows + per_block - 1) / per_block;
+    share_blocks(a, p->D, 5 * 148, 4);
     const uint32_t blocks = a.blocks_q + a.blocks_k;
     if (blocks == 0) return SLIKL_OK;
     auto kernel = p->dtype == SLIKL_BF16
@@ -632,17 +829,7 @@ slikl_status run_gradient(const slikl_qk_problem *p, const slikl_qk_tensors *t, 
                           cudaStream_t st) {
     Args a = make_args(p, t);
     a.partial = partial;
-    const uint32_t tile = (kThreads / 32) * (uint32_t)(512 / p->D);
-    const uint32_t tq = (a.side[0].rows + tile - 1) / tile, tk = (a.side[1].rows + tile - 1) / tile;
-    const uint32_t most = 296;       // two blocks on each multiprocessor
-    if (tq + tk <= most) {
-        a.blocks_q = tq;
-        a.blocks_k = tk;
-    } else {                         // in proportion to the work, one at least for a side with rows
-        const uint32_t share = (uint32_t)((uint64_t)most * tk / ((uint64_t)tq + tk));
-        a.blocks_k = tk == 0 ? 0 : std::min(tk, std::max(share, 1u));
-        a.blocks_q = std::min(tq, most - a.blocks_k);
-    }
+    share_blocks(a, p->D, 4 * 148, 6);
     if (a.blocks_q + a.blocks_k > 0) {
         auto kernel =
             p->dtype == SLIKL_BF16

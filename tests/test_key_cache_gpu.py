@@ -256,8 +256,8 @@ def test_evict(case, kind):
     lead = (B, lens[0]) if bsnd else (total,)
     outs = [torch.full((B, budget, *c.shape[1:]), 3, dtype=c.dtype, device="cuda") for c in caches]
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
-    r = sli.evict(dev(scores).reshape(lead), [dev(c).reshape(*lead, *c.shape[1:]) for c in caches], budget, sinks, recent,
-                  layout_k=layout, cu_seqlens_k=None if bsnd else dev(cu(lens)),
+    r = sli.evict(dev(scores).reshape(lead), [dev(c).reshape(*lead, *c.shape[1:]) for c in caches], budget,
+                  sinks=sinks, recent=recent, layout_k=layout, cu_seqlens_k=None if bsnd else dev(cu(lens)),
                   seq_used_k=None if used is None else torch.tensor(used, dtype=torch.int32, device="cuda"),
                   out=dict(caches=outs), status=status)
     assert int(status) == 0
@@ -357,11 +357,11 @@ def test_graph_and_other_stream():
     i, w, s = dev(idx).reshape(1, 64, 1, K), dev(w).reshape(1, 64, 1, K), torch.rand(1, 3000, device="cuda")
     c = torch.randn(1, 3000, 64, device="cuda")
     want = sli.key_weights(w, i, s)["scores"]
-    cut = sli.evict(want, [c], 500, 4, 8)
+    cut = sli.evict(want, [c], 500, sinks=4, recent=8)
     torch.cuda.synchronize()
     st = torch.cuda.Stream()
     a = sli.key_weights(w, i, s, stream=st)["scores"]
-    b = sli.evict(a, [c], 500, 4, 8, stream=st)
+    b = sli.evict(a, [c], 500, sinks=4, recent=8, stream=st)
     st.synchronize()
     assert torch.equal(a, want) and torch.equal(b["kept"], cut["kept"]) and torch.equal(b["caches"][0], cut["caches"][0])
     ws = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
@@ -370,13 +370,13 @@ def test_graph_and_other_stream():
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
             a = sli.key_weights(w * scale, i, s, workspace=ws)["scores"]
-            b = sli.evict(a, [c], 500, 4, 8)
+            b = sli.evict(a, [c], 500, sinks=4, recent=8)
         graphs.append((g, a, b, scale))
     for j in (0, 1, 1, 0):
         graphs[j][0].replay()
     torch.cuda.synchronize()
     for _, a, b, scale in graphs:
         want = sli.key_weights(w * scale, i, s)["scores"]
-        cut = sli.evict(want, [c], 500, 4, 8)
+        cut = sli.evict(want, [c], 500, sinks=4, recent=8)
         assert torch.equal(a, want) and torch.equal(b["kept"], cut["kept"])
         assert torch.equal(b["caches"][0], cut["caches"][0])
