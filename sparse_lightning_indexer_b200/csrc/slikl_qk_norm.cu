@@ -52,6 +52,8 @@ __device__ __forceinline__ uint32_t div_by(uint32_t n, const FastDiv &f) {
 
 struct Side {
     uint32_t rows;            // head rows T * N
+    uint32_t per_warp, longer;   // groups of rows of each warp; one more for the first `longer`
+    int two;                  // groups of two rows a thread, all of one token
     FastDiv N, S;
     int norm;
     uint32_t x_stride, dx_stride;   // bytes from one row to the next
@@ -80,7 +82,10 @@ struct Args {
 };
 
 constexpr int kThreads = 128;
-constexpr int kGradBlocks = 1024;     // most blocks of the gradient kernel (the workspace's size)
+constexpr int kFwdPerSm = 6, kGradPerSm = 4;   // blocks that a multiprocessor's registers hold
+constexpr int kMaxSms = 256;
+constexpr int kGradBlocks = kMaxSms * kGradPerSm;   // most blocks of the gradient kernel (the
+                                                    // workspace's size)
 
 // What one thread of a head row is responsible for.
 struct Lane {
@@ -142,6 +147,55 @@ __device__ __forceinline__ void load_angles(const Args &a, const Lane &t, int32_
         const float4 s = *reinterpret_cast<const float4 *>(row + a.rot / 2 + (h ? t.tb : t.ta));
         g.c[2 * h] = pair(c.x, c.y), g.c[2 * h + 1] = pair(c.z, c.w);
         g.s[2 * h] = pair(s.x, s.y), g.s[2 * h + 1] = pair(s.z, s.w);
+    }
+}
+
+// What turns scaled values and applies the gain in one go, v -> v c + w s with w the value's partner
+// in the rotation, formed once a token: c the gain times the cosine, s the partner's gain times
+// plus or minus the sine (1 and 0 where nothing turns).
+struct Turner {
+    Pair c[8], s[8];
+};
+
+__device__ __forceinline__ Pair swapped(Pair p) { return pair(p.f.y, p.f.x); }
+
+__device__ __forceinline__ void form_turner(const Args &a, const Lane &t, const Pair *gain,
+                                            int32_t pos, Turner &o) {
+    Angles g;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) g.c[i] = pair(1.f, 1.f), g.s[i] = pair(0.f, 0.f);
+    if (t.turns) load_angles(a, t, pos, g);
+    if (a.pairs) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float c = i & 1 ? g.c[i / 2].f.y : g.c[i / 2].f.x;
+            const float s = i & 1 ? g.s[i / 2].f.y : g.s[i / 2].f.x;
+            o.c[i] = gain[i] * pair(c, c);
+            o.s[i] = swapped(gain[i]) * pair(-s, s);
+        }
+    } else {
+        const Pair minus = pair(-1.f, -1.f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            o.c[i] = gain[i] * g.c[i];
+            o.c[i + 4] = gain[i + 4] * g.c[i];
+            o.s[i] = gain[i + 4] * g.s[i] * minus;
+            o.s[i + 4] = gain[i] * g.s[i];
+        }
+    }
+}
+
+__device__ __forceinline__ void turn(Pair *v, const Turner &o, int pairs) {
+    if (pairs) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = fma2(v[i], o.c[i], swapped(v[i]) * o.s[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const Pair x = v[i], y = v[i + 4];
+            v[i] = fma2(x, o.c[i], y * o.s[i]);
+            v[i + 4] = fma2(y, o.c[i + 4], x * o.s[i + 4]);
+        }
     }
 }
 
@@ -217,24 +271,39 @@ __device__ __forceinline__ float row_max(float v) {
     return v;
 }
 
+// Two sums at once, so that one's shuffles fill the other's latency.
+template <int TPR>
+__device__ __forceinline__ void row_sums(float &v, float &w) {
+#pragma unroll
+    for (int o = TPR / 2; o > 0; o >>= 1) {
+        const float x = __shfl_xor_sync(0xffffffffu, v, o), y = __shfl_xor_sync(0xffffffffu, w, o);
+        v += x;
+        w += y;
+    }
+}
+// Sums over the thread's values, as two running ones.
+__device__ __forceinline__ Pair sum8(const Pair *v) {
+    return ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+}
+__device__ __forceinline__ Pair dot8(const Pair *v, const Pair *w) {
+    Pair a = v[0] * w[0], b = v[1] * w[1];
+#pragma unroll
+    for (int i = 2; i < 8; i += 2) a = fma2(v[i], w[i], a), b = fma2(v[i + 1], w[i + 1], b);
+    return a + b;
+}
+
 // Takes the row's mean off x (layer norm) and returns r. The variance is taken about the mean, not
 // as a difference of moments, so that a mean far above the deviation costs no digits.
 template <int D, int NORM>
 __device__ __forceinline__ float centre(Pair *x, float eps) {
     constexpr int TPR = D / 16;
     if (NORM == SLIKL_NORM_LAYER) {
-        Pair m = x[0];
-#pragma unroll
-        for (int i = 1; i < 8; ++i) m = m + x[i];
-        const float mean = row_sum<TPR>(both(m)) * (-1.f / D);
+        const float mean = row_sum<TPR>(both(sum8(x))) * (-1.f / D);
         const Pair less = pair(mean, mean);
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = x[i] + less;
     }
-    Pair q = x[0] * x[0];
-#pragma unroll
-    for (int i = 1; i < 8; ++i) q = fma2(x[i], x[i], q);
-    return rsqrtf(fmaf(row_sum<TPR>(both(q)), 1.f / D, eps));
+    return rsqrtf(fmaf(row_sum<TPR>(both(dot8(x, x))), 1.f / D, eps));
 }
 
 __device__ __forceinline__ void cp_async8(uint32_t dst, const void *src) {
@@ -247,122 +316,155 @@ __device__ __forceinline__ void cp_async_commit() {
     asm volatile("cp.async.commit_group;" ::: "memory");
 }
 
-// A stage of the threads' rings: a row of x (two 16-byte chunks, or two 8-byte ones and the scale of
-// a checkpoint), of dy (two 16-byte chunks) and its position. Neighbouring threads' chunks are
-// neighbours, so no access has a bank conflict.
-template <bool SRC8, bool GRAD>
+// A stage of the threads' rings: U rows of x (two 16-byte chunks each, or two 8-byte ones and the
+// scale of a checkpoint) and of dy (two 16-byte chunks), and their position. Neighbouring threads'
+// chunks are neighbours, so no access has a bank conflict.
+template <bool SRC8, bool GRAD, int U>
 struct Stage {
-    uint4 x[SRC8 ? 1 : 2][kThreads];       // (a checkpoint's two 8-byte chunks are x[0][i])
-    uint4 dy[GRAD ? 2 : 1][GRAD ? kThreads : 1];
-    float scale[SRC8 ? kThreads : 1];
-    int32_t pos[kThreads];                 // -1: the row takes no part
+    uint4 x[U][SRC8 ? 1 : 2][kThreads];    // (a checkpoint's two 8-byte chunks are x[u][0][i])
+    uint4 dy[GRAD ? U : 1][GRAD ? 2 : 1][GRAD ? kThreads : 1];
+    float scale[SRC8 ? U : 1][SRC8 ? kThreads : 1];
+    int32_t pos[kThreads];                 // -1: the rows take no part, and their values are zero
 };
-constexpr int kStages = 4;
-template <bool SRC8, bool GRAD>
-using Ring = Stage<SRC8, GRAD>[kStages];
+// Rows a thread has on the way beside those it works on: three one at a time, four (forward) or two
+// (gradient: x and dy of each) two at a time.
+template <bool GRAD, int U>
+constexpr int kStages = U == 1 ? 4 : GRAD ? 2 : 3;
+template <bool SRC8, bool GRAD, int U>
+using Ring = Stage<SRC8, GRAD, U>[kStages<GRAD, U>];
+template <bool GRAD>
+constexpr size_t kRingBytes = std::max({sizeof(Ring<false, GRAD, 1>), sizeof(Ring<true, GRAD, 1>),
+                                        sizeof(Ring<false, GRAD, 2>), sizeof(Ring<true, GRAD, 2>)});
 
-// The rows of a warp: groups of RPW = 512 / D rows next to one another, an equal share of the
-// side's groups. `row` is the thread's row in the group, which it steps through together with its
-// token and head; rows behind the side's last one are worked on like the others, but neither read
-// nor stored.
-template <int RPW>
+// The rows of a warp: groups of U * RPW rows next to one another (RPW = 512 / D), an equal share of
+// the side's groups. `row` is the thread's (first) row in the group, which it steps through together
+// with its token and head; its second one, with U = 2, is RPW rows on and of the same token: that
+// form is taken where a token's heads are a multiple of 2 * RPW, and shares the work that is not
+// arithmetic, more than half of a plain copy's 145 instructions, between two rows. Rows behind the
+// side's last one are worked on like padding, and not stored.
+template <int RPW, int U>
 struct Walk {
     uint32_t row, token, head;
     int32_t steps;
-    uint32_t dt, dh;          // a step of RPW rows is dt tokens and dh heads
-    __device__ __forceinline__ Walk(const Side &s, uint32_t block, uint32_t blocks, int sub) {
-        const uint32_t groups = (s.rows + RPW - 1) / RPW;
+    uint32_t dt, dh;          // a step is dt tokens and dh heads
+    __device__ __forceinline__ Walk(const Side &s, uint32_t block, int sub) {
         const uint32_t warp = block * (kThreads / 32) + (threadIdx.x >> 5);
-        const uint32_t warps = blocks * (kThreads / 32);
-        const uint32_t begin = (uint32_t)((uint64_t)groups * warp / warps);
-        steps = (int32_t)((uint32_t)((uint64_t)groups * (warp + 1) / warps) - begin);
-        row = begin * RPW + sub;
+        steps = (int32_t)(s.per_warp + (warp < s.longer));
+        row = (warp * s.per_warp + min(warp, s.longer)) * (RPW * U) + sub;
         token = div_by(row, s.N);
         head = row - token * s.N.d;
-        dt = div_by(RPW, s.N);
-        dh = RPW - dt * s.N.d;
+        dt = U == 2 ? 0 : div_by(RPW, s.N);
+        dh = U == 2 ? 2 * RPW : RPW - dt * s.N.d;
     }
-    __device__ __forceinline__ void step(const Side &s) {
-        row += RPW;
-        token += dt;
+    // Whether the step led to another token.
+    __device__ __forceinline__ bool step(const Side &s) {
+        row += RPW * U;
+        if (U == 1) token += dt;
         head += dh;
-        if (head >= s.N.d) {
-            head -= s.N.d;
-            ++token;
-        }
+        if (head < s.N.d) return U == 1 && dt != 0;
+        head -= s.N.d;
+        ++token;
+        return true;
     }
 };
 
-// Copies the rows to come into the ring.
-template <typename T, int D, bool SRC8, bool GRAD, bool READS_X>
+// Copies the rows to come into the ring. Rows that take no part arrive as zeros, so that the work on
+// them needs no branches: their y, checkpoint and dx come out as zero and they add zero to every sum.
+template <typename T, int D, bool SRC8, bool GRAD, bool READS_X, int U>
 struct Fetch {
-    Walk<512 / D> w;
+    static constexpr int RPW = 512 / D;
+    Walk<RPW, U> w;
     const char *x, *dy;       // the thread's first chunk of row 0
-    int32_t pos, last;        // the walk's position, read a step early, and the one before
+    int32_t pos;              // of the walk's token, read a step early; -1: takes no part
+    bool fresh;               // not looked at yet
     uint32_t stage;
 
     __device__ __forceinline__ Fetch(const Args &a, const Side &s, const Lane &t,
-                                     const Walk<512 / D> &from)
-        : w(from), last(-1), stage(0) {
+                                     const Walk<RPW, U> &from)
+        : w(from), stage(0) {
         x = SRC8 ? reinterpret_cast<const char *>(s.x8) + t.ca
                  : static_cast<const char *>(s.x) + 2 * t.ca;
         dy = static_cast<const char *>(s.dy) + 2 * t.ca;
-        find_position(a, s);
+        find_position(s);
     }
-    // The row's position, -1 where it takes no part; a bad one is flagged.
-    __device__ __forceinline__ void find_position(const Args &a, const Side &s) {
+    __device__ __forceinline__ void find_position(const Side &s) {
         pos = -1;
-        if (w.row >= s.rows) return;
-        pos = s.positions ? s.positions[w.token]
-                          : (int32_t)(w.token - div_by(w.token, s.S) * s.S.d);
+        fresh = true;
+        if (w.row < s.rows)
+            pos = s.positions ? s.positions[w.token]
+                              : (int32_t)(w.token - div_by(w.token, s.S) * s.S.d);
     }
-    // Starts the copies of the walk's row, brings its angles near, and steps on. (A row's angles are
-    // loaded when it is worked on, often once for many heads; keys of one head need new ones each
-    // row, and without the prefetch their side took twice as long as the queries'.)
-    __device__ __forceinline__ void next(Ring<SRC8, GRAD> &ring, const Args &a, const Side &s,
+    // Starts the copies of the walk's rows and steps on. A token's position is checked, a bad one
+    // flagged, and its angles are brought near, once. (They are loaded when the row is worked on, often
+    // once for many heads; keys of one head need new ones each row, and without the prefetch their
+    // side took twice as long as the queries'.)
+    __device__ __forceinline__ void next(Ring<SRC8, GRAD, U> &ring, const Args &a, const Side &s,
                                          const Lane &t) {
-        Stage<SRC8, GRAD> &to = ring[stage];
-        stage = (stage + 1) % kStages;
+        auto &to = ring[stage];
+        if (++stage == kStages<GRAD, U>) stage = 0;
         const int i = threadIdx.x;
-        if (pos < 0 || (a.rot && (uint32_t)pos >= a.table_rows)) {
-            if (pos != -1 && a.status) set_status(a.status, SLIKL_DEV_BAD_POSITION);
-            pos = -1;
-        } else if (t.turns && pos != last) {
-            const float *row = a.cos_sin + (int64_t)pos * a.rot + t.ta;
-            asm volatile("prefetch.global.L1 [%0];" ::"l"(row));
-            asm volatile("prefetch.global.L1 [%0];" ::"l"(row + a.rot / 2));
+        if (fresh) {
+            fresh = false;
+            if (pos < 0 || (a.rot && (uint32_t)pos >= a.table_rows)) {
+                if (pos != -1 && a.status) set_status(a.status, SLIKL_DEV_BAD_POSITION);
+                pos = -1;
+            } else if (t.turns) {
+                const float *row = a.cos_sin + (int64_t)pos * a.rot + t.ta;
+                asm volatile("prefetch.global.L1 [%0];" ::"l"(row));
+                asm volatile("prefetch.global.L1 [%0];" ::"l"(row + a.rot / 2));
+            }
         }
-        to.pos[i] = last = pos;
-        if (w.row < s.rows) {
+        to.pos[i] = pos;
+        const uint32_t apart = t.cb - t.ca;
+        if (pos >= 0) {                        // (never behind the last row)
             if (READS_X && SRC8) {
                 const char *p = x + (uint64_t)w.row * D;
-                const uint32_t at = sm100::smem_u32(&to.x[0][i]);
-                cp_async8(at, p);
-                cp_async8(at + 8, p + (t.cb - t.ca));
-                cp_async4(sm100::smem_u32(&to.scale[i]), s.x8_scale + w.row);
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const uint32_t at = sm100::smem_u32(&to.x[u][0][i]);
+                    cp_async8(at, p + u * RPW * D);
+                    cp_async8(at + 8, p + u * RPW * D + apart);
+                    cp_async4(sm100::smem_u32(&to.scale[u][i]), s.x8_scale + w.row + u * RPW);
+                }
             } else if (READS_X) {
                 const char *p = x + (uint64_t)w.token * s.x_stride + w.head * (2 * D);
-                sm100::cp_async16(sm100::smem_u32(&to.x[0][i]), p, 16);
-                sm100::cp_async16(sm100::smem_u32(&to.x[SRC8 ? 0 : 1][i]), p + 2 * (t.cb - t.ca), 16);
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    sm100::cp_async16(sm100::smem_u32(&to.x[u][0][i]), p + u * RPW * 2 * D, 16);
+                    sm100::cp_async16(sm100::smem_u32(&to.x[u][SRC8 ? 0 : 1][i]),
+                                      p + u * RPW * 2 * D + 2 * apart, 16);
+                }
             }
             if (GRAD) {
                 const char *p = dy + (uint64_t)w.row * (2 * D);
-                sm100::cp_async16(sm100::smem_u32(&to.dy[0][i]), p, 16);
-                sm100::cp_async16(sm100::smem_u32(&to.dy[GRAD ? 1 : 0][i]), p + 2 * (t.cb - t.ca), 16);
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    sm100::cp_async16(sm100::smem_u32(&to.dy[GRAD ? u : 0][0][i]), p + u * RPW * 2 * D, 16);
+                    sm100::cp_async16(sm100::smem_u32(&to.dy[GRAD ? u : 0][GRAD ? 1 : 0][i]),
+                                      p + u * RPW * 2 * D + 2 * apart, 16);
+                }
+            }
+        } else {
+            const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                to.x[u][0][i] = zero;
+                if (SRC8) to.scale[SRC8 ? u : 0][SRC8 ? i : 0] = 0.f;
+                else to.x[u][SRC8 ? 0 : 1][i] = zero;
+                if (GRAD) to.dy[GRAD ? u : 0][0][GRAD ? i : 0] = to.dy[GRAD ? u : 0][GRAD ? 1 : 0][GRAD ? i : 0] = zero;
             }
         }
         cp_async_commit();
-        w.step(s);
-        find_position(a, s);
+        if (w.step(s)) find_position(s);
     }
 };
 
-template <typename T, bool SRC8, bool GRAD>
-__device__ __forceinline__ void source(const Stage<SRC8, GRAD> &from, Pair *v) {
+template <typename T, bool SRC8, bool GRAD, int U>
+__device__ __forceinline__ void source(const Stage<SRC8, GRAD, U> &from, int u, Pair *v) {
     const int i = threadIdx.x;
-    const uint4 x = from.x[0][i];
-    if (SRC8) widen8(make_uint2(x.x, x.y), make_uint2(x.z, x.w), from.scale[SRC8 ? i : 0], v);
-    else widen<T>(x, from.x[SRC8 ? 0 : 1][i], v);
+    const uint4 x = from.x[u][0][i];
+    if (SRC8) widen8(make_uint2(x.x, x.y), make_uint2(x.z, x.w), from.scale[SRC8 ? u : 0][SRC8 ? i : 0], v);
+    else widen<T>(x, from.x[u][SRC8 ? 0 : 1][i], v);
 }
 
 __device__ __forceinline__ void load16(const float *p, const Lane &t, Pair *v) {
@@ -401,23 +503,20 @@ __device__ __forceinline__ uint32_t top_of<__half>(const uint4 &a, const uint4 &
 // that are not `in` are not stored. `top`: top_of the thread's values.
 template <typename T, int D>
 __device__ __forceinline__ void keep_row(const Side &s, uint32_t row, const Lane &t, int l,
-                                         bool in, bool live, uint32_t top, const Pair *x) {
+                                         bool in, uint32_t top, const Pair *x) {
     const float2 two = unpack2<T>(top);
     const float m = row_max<D / 16>(fmaxf(two.x, two.y));
     if (!in) return;
     // a row of subnormal bf16 values keeps a normal scale, so that its reciprocal is finite
-    const bool some = live && m > 0.f;
-    const float scale = some ? fmaxf(m * (1.f / 448.f), FLT_MIN) : 0.f;
-    const float inv = some ? __fdividef(1.f, scale) : 0.f;
-    uint32_t w[4] = {0, 0, 0, 0};
-    if (live) {
-        const Pair by = pair(inv, inv);
+    const float scale = m > 0.f ? fmaxf(m * (1.f / 448.f), FLT_MIN) : 0.f;
+    const float inv = m > 0.f ? __fdividef(1.f, scale) : 0.f;
+    const Pair by = pair(inv, inv);
+    uint32_t w[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t lo = __nv_cvt_float2_to_fp8x2((x[2 * i] * by).f, __NV_SATFINITE, __NV_E4M3);
-            const uint32_t hi = __nv_cvt_float2_to_fp8x2((x[2 * i + 1] * by).f, __NV_SATFINITE, __NV_E4M3);
-            w[i] = __byte_perm(lo, hi, 0x5410);
-        }
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2((x[2 * i] * by).f, __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi = __nv_cvt_float2_to_fp8x2((x[2 * i + 1] * by).f, __NV_SATFINITE, __NV_E4M3);
+        w[i] = __byte_perm(lo, hi, 0x5410);
     }
     uint8_t *p = s.keep8 + t.ca + (uint64_t)row * D;
     *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
@@ -425,172 +524,209 @@ __device__ __forceinline__ void keep_row(const Side &s, uint32_t row, const Lane
     if (l == 0) s.keep8_scale[row] = scale;
 }
 
-template <typename T, int D, int NORM, bool SRC8>
+template <typename T, int D, int NORM, bool SRC8, int U>
 __device__ __forceinline__ void forward_rows(const Args &a, const Side &s, uint32_t block,
-                                             uint32_t blocks, void *smem) {
+                                             void *smem) {
     constexpr int TPR = D / 16, RPW = 32 / TPR;
-    auto &ring = *static_cast<Ring<SRC8, false> *>(smem);
+    auto &ring = *static_cast<Ring<SRC8, false, U> *>(smem);
     const int l = (threadIdx.x & 31) % TPR;
     const Lane t = lane_of(l, a.rot, a.pairs, D);
-    const Walk<RPW> walk(s, block, blocks, (threadIdx.x & 31) / TPR);
+    const Walk<RPW, U> walk(s, block, (threadIdx.x & 31) / TPR);
     const int32_t steps = walk.steps;
     uint32_t row = walk.row, stage = 0;
-    Fetch<T, D, SRC8, false, true> fetch(a, s, t, walk);
+    Fetch<T, D, SRC8, false, true, U> fetch(a, s, t, walk);
 #pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) {
+    for (int i = 0; i < kStages<false, U> - 1; ++i) {
         if (i < steps) fetch.next(ring, a, s, t);
         else cp_async_commit();
     }
-    Pair gain[8];
+    // without a bias the gain goes into the rotation, and both together into a Turner; a layer norm
+    // (of keys of one head, mostly) takes gain, bias and angles one after another
+    constexpr bool LAYER = NORM == SLIKL_NORM_LAYER;
+    Turner turner;
     Angles angles;
-    int32_t turned_to = -1;               // the position that `angles` belongs to
-    if (NORM != SLIKL_NORM_NONE && s.gain) load16(s.gain, t, gain);
-    for (int32_t i = 0; i < steps; ++i, row += RPW) {
-        sm100::cp_async_wait<kStages - 2>();
-        const Stage<SRC8, false> &now = ring[stage];
-        stage = (stage + 1) % kStages;
+    int32_t turned_to = -1;               // the position that they belong to
+#pragma unroll
+    for (int j = 0; j < 8; ++j) turner.c[j] = turner.s[j] = pair(0.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) angles.c[j] = angles.s[j] = pair(0.f, 0.f);
+    for (int32_t i = 0; i < steps; ++i, row += RPW * U) {
+        sm100::cp_async_wait<kStages<false, U> - 2>();
+        const auto &now = ring[stage];
+        if (++stage == kStages<false, U>) stage = 0;
         const int32_t pos = now.pos[threadIdx.x];
-        const bool in = row < s.rows, live = pos >= 0;
-        if (live && t.turns && pos != turned_to) {
-            load_angles(a, t, pos, angles);
+        if (pos >= 0 && pos != turned_to) {
             turned_to = pos;
-        }
-        Pair v[8];
-        source<T>(now, v);
-        uint32_t top = 0;
-        if (!SRC8 && s.keep8) top = top_of<T>(now.x[0][threadIdx.x], now.x[SRC8 ? 0 : 1][threadIdx.x]);
-        if (i + kStages - 1 < steps) fetch.next(ring, a, s, t);
-        else cp_async_commit();
-        if (!SRC8 && s.keep8) keep_row<T, D>(s, row, t, l, in, live, top, v);
-        if (!s.y) continue;
-        if (NORM != SLIKL_NORM_NONE) {
-            const float r = centre<D, NORM>(v, a.eps);
-            const Pair by = pair(r, r);
+            if (LAYER) {
+                if (t.turns) load_angles(a, t, pos, angles);
+            } else {
+                Pair gain[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = v[j] * by;
-            if (s.gain) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = v[j] * gain[j];
+                for (int j = 0; j < 8; ++j) gain[j] = pair(1.f, 1.f);
+                if (s.gain) load16(s.gain, t, gain);
+                form_turner(a, t, gain, pos, turner);
             }
         }
-        if (NORM == SLIKL_NORM_LAYER && s.bias) {
-            Pair bias[8];
-            load16(s.bias, t, bias);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = v[j] + bias[j];
-        }
-        if (!in) continue;
+        if (i + kStages<false, U> - 1 < steps) fetch.next(ring, a, s, t);
+        else cp_async_commit();
         char *y = static_cast<char *>(s.y) + 2 * t.ca + (uint64_t)row * (2 * D);
-        if (!live) {
-            zero_store(y, t);
-            continue;
+        const bool in = U == 2 || row < s.rows;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            Pair v[8];
+            source<T>(now, u, v);
+            if (!SRC8 && s.keep8)
+                keep_row<T, D>(s, row + u * RPW, t, l, in,
+                               top_of<T>(now.x[u][0][threadIdx.x], now.x[u][SRC8 ? 0 : 1][threadIdx.x]), v);
+            if (!s.y) continue;
+            if (NORM != SLIKL_NORM_NONE) {
+                const float r = centre<D, NORM>(v, a.eps);
+                const Pair by = pair(r, r);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = v[j] * by;
+            }
+            if (!in) continue;
+            if (LAYER) {
+                if (pos < 0) {            // the bias is not zero
+                    zero_store(y + u * RPW * 2 * D, t);
+                    continue;
+                }
+                if (s.gain) {
+                    Pair gain[8];
+                    load16(s.gain, t, gain);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] = v[j] * gain[j];
+                }
+                if (s.bias) {
+                    Pair bias[8];
+                    load16(s.bias, t, bias);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] = v[j] + bias[j];
+                }
+                if (t.turns) turn<false>(v, angles, a.pairs);
+            } else if (NORM != SLIKL_NORM_NONE || a.rot) {
+                turn(v, turner, a.pairs);
+            }
+            narrow_store<T>(y + u * RPW * 2 * D, t, v);
         }
-        if (t.turns) turn<false>(v, angles, a.pairs);
-        narrow_store<T>(y, t, v);
     }
 }
 
-template <typename T, int D, bool SRC8>
+template <typename T, int D, bool SRC8, int U>
 __device__ __forceinline__ void forward_side(const Args &a, const Side &s, uint32_t block,
-                                             uint32_t blocks, void *smem) {
+                                             void *smem) {
     if (s.norm == SLIKL_NORM_RMS)
-        forward_rows<T, D, SLIKL_NORM_RMS, SRC8>(a, s, block, blocks, smem);
+        forward_rows<T, D, SLIKL_NORM_RMS, SRC8, U>(a, s, block, smem);
     else if (s.norm == SLIKL_NORM_LAYER)
-        forward_rows<T, D, SLIKL_NORM_LAYER, SRC8>(a, s, block, blocks, smem);
+        forward_rows<T, D, SLIKL_NORM_LAYER, SRC8, U>(a, s, block, smem);
     else
-        forward_rows<T, D, SLIKL_NORM_NONE, SRC8>(a, s, block, blocks, smem);
+        forward_rows<T, D, SLIKL_NORM_NONE, SRC8, U>(a, s, block, smem);
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, 5) qk_forward(const __grid_constant__ Args a) {
-    __shared__ __align__(16) unsigned char smem[sizeof(Ring<false, false>)];
-    static_assert(sizeof(Ring<true, false>) <= sizeof(smem), "ring of a checkpoint");
+__global__ void __launch_bounds__(kThreads, kFwdPerSm) qk_forward(const __grid_constant__ Args a) {
+    __shared__ __align__(16) unsigned char smem[kRingBytes<false>];
     const bool k = blockIdx.x >= a.blocks_q;
     const Side &s = a.side[k];
-    const uint32_t block = blockIdx.x - (k ? a.blocks_q : 0), blocks = k ? a.blocks_k : a.blocks_q;
-    if (s.x) forward_side<T, D, false>(a, s, block, blocks, smem);
-    else forward_side<T, D, true>(a, s, block, blocks, smem);
+    const uint32_t block = blockIdx.x - (k ? a.blocks_q : 0);
+    if (s.x) {
+        if (s.two) forward_side<T, D, false, 2>(a, s, block, smem);
+        else forward_side<T, D, false, 1>(a, s, block, smem);
+    } else {
+        if (s.two) forward_side<T, D, true, 2>(a, s, block, smem);
+        else forward_side<T, D, true, 1>(a, s, block, smem);
+    }
 }
 
 // Gradient: the sums of dgain and dbias stay in registers over a warp's rows, are added over the
 // block in a fixed order and stored; qk_grad_sums adds the blocks' sums, again in a fixed order.
-// With x less its mean, e = dz r and u = e gain:
-//   dgain += e x,  dbias += dz,  dx = u - x r^2 mean(u x) - mean(u)      (the last for layer only)
-template <typename T, int D, int NORM, bool SRC8>
+// With x less its mean, h = dz gain:
+//   dbias += dz,  dgain += dz (x r),  dx = r (h - [mean(h)]) - (x r) r^2 mean(h x)
+template <typename T, int D, int NORM, bool SRC8, int U>
 __device__ __forceinline__ void gradient_rows(const Args &a, const Side &s, uint32_t block,
-                                              uint32_t blocks, float *partial, void *ring_smem) {
+                                              float *partial, void *ring_smem) {
     constexpr int TPR = D / 16, RPW = 32 / TPR, WARPS = kThreads / 32;
     constexpr bool X = NORM != SLIKL_NORM_NONE;        // without a norm x is not needed
-    auto &ring = *static_cast<Ring<SRC8, true> *>(ring_smem);
+    constexpr bool LAYER = NORM == SLIKL_NORM_LAYER;
+    auto &ring = *static_cast<Ring<SRC8, true, U> *>(ring_smem);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const Lane t = lane_of(lane % TPR, a.rot, a.pairs, D);
-    Walk<RPW> at(s, block, blocks, lane / TPR);
+    Walk<RPW, U> at(s, block, lane / TPR);
     const int32_t steps = at.steps;
     uint32_t stage = 0;
-    Fetch<T, D, SRC8, true, X> fetch(a, s, t, at);
+    Fetch<T, D, SRC8, true, X, U> fetch(a, s, t, at);
 #pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) {
+    for (int i = 0; i < kStages<true, U> - 1; ++i) {
         if (i < steps) fetch.next(ring, a, s, t);
         else cp_async_commit();
     }
     Pair gain[8], dgain[8], dbias[8];
     Angles angles;
     int32_t turned_to = -1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) angles.c[i] = angles.s[i] = pair(0.f, 0.f);
     if (X) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) gain[i] = pair(1.f, 1.f), dgain[i] = dbias[i] = pair(0.f, 0.f);
         if (s.gain) load16(s.gain, t, gain);
     }
     for (int32_t i = 0; i < steps; ++i, at.step(s)) {
-        sm100::cp_async_wait<kStages - 2>();
-        const Stage<SRC8, true> &now = ring[stage];
-        stage = (stage + 1) % kStages;
+        sm100::cp_async_wait<kStages<true, U> - 2>();
+        const auto &now = ring[stage];
+        if (++stage == kStages<true, U>) stage = 0;
         const int32_t pos = now.pos[threadIdx.x];
-        const bool in = at.row < s.rows, live = pos >= 0;
-        if (live && t.turns && pos != turned_to) {
+        if (t.turns && pos >= 0 && pos != turned_to) {
             load_angles(a, t, pos, angles);
             turned_to = pos;
         }
-        Pair g[8], v[8];
-        widen<T>(now.dy[0][threadIdx.x], now.dy[1][threadIdx.x], g);
-        if (X) source<T>(now, v);
-        if (i + kStages - 1 < steps) fetch.next(ring, a, s, t);
+        if (i + kStages<true, U> - 1 < steps) fetch.next(ring, a, s, t);
         else cp_async_commit();
-        if (live && t.turns) turn<true>(g, angles, a.pairs);
-        if (X) {
-            const float r = centre<D, NORM>(v, a.eps);
-            const Pair by = pair(r, r);
-            if (live) {                   // (rows behind the last one are at position -1)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    if (NORM == SLIKL_NORM_LAYER) dbias[j] = dbias[j] + g[j];
-                    g[j] = g[j] * by;
-                    dgain[j] = fma2(g[j], v[j], dgain[j]);
-                }
-            }
-            Pair su, sv;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                g[j] = g[j] * gain[j];
-                su = j ? su + g[j] : g[j];
-                sv = j ? fma2(g[j], v[j], sv) : g[j] * v[j];
-            }
-            const float m = row_sum<TPR>(both(sv)) * (r * r * (-1.f / D));
-            const Pair along = pair(m, m);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) g[j] = fma2(v[j], along, g[j]);
-            if (NORM == SLIKL_NORM_LAYER) {
-                const float l = row_sum<TPR>(both(su)) * (-1.f / D);
-                const Pair less = pair(l, l);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) g[j] = g[j] + less;
-            }
-        }
-        if (!in) continue;
         char *dx = static_cast<char *>(s.dx) + 2 * t.ca + (uint64_t)at.token * s.dx_stride +
                    at.head * (2 * D);
-        if (live) narrow_store<T>(dx, t, g);
-        else zero_store(dx, t);
+#pragma unroll 1
+        for (int u = 0; u < U; ++u) {      // (two rows at once would not fit the registers)
+            Pair g[8], v[8];
+            widen<T>(now.dy[u][0][threadIdx.x], now.dy[u][1][threadIdx.x], g);
+            if (X) source<T>(now, u, v);
+            if (t.turns) turn<true>(g, angles, a.pairs);
+            if (X) {
+                // two rounds of sums over the row's threads, each of two sums side by side: the means
+                // of x and h (layer only), then x^2 and h x
+                float lift = 0.f;
+                if (LAYER) {
+                    Pair sum = g[0] * gain[0];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        if (j) sum = fma2(g[j], gain[j], sum);
+                        dbias[j] = dbias[j] + g[j];
+                    }
+                    float sx = both(sum8(v)), sh = both(sum);
+                    row_sums<TPR>(sx, sh);
+                    lift = sh * (-1.f / D);
+                    const Pair less = pair(sx * (-1.f / D), sx * (-1.f / D));
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] = v[j] + less;
+                }
+                Pair sum = (g[0] * gain[0]) * v[0], more = (g[1] * gain[1]) * v[1];
+#pragma unroll
+                for (int j = 2; j < 8; j += 2) {
+                    sum = fma2(g[j] * gain[j], v[j], sum);
+                    more = fma2(g[j + 1] * gain[j + 1], v[j + 1], more);
+                }
+                float sq = both(dot8(v, v)), sh = both(sum + more);
+                row_sums<TPR>(sq, sh);
+                const float r = rsqrtf(fmaf(sq, 1.f / D, a.eps)), m = sh * (r * r * (-1.f / D));
+                const Pair by = pair(r, r), along = pair(m, m), up = pair(lift, lift);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    v[j] = v[j] * by;
+                    dgain[j] = fma2(g[j], v[j], dgain[j]);
+                    const Pair h = LAYER ? fma2(g[j], gain[j], up) : g[j] * gain[j];
+                    g[j] = fma2(h, by, v[j] * along);
+                }
+            }
+            if (U == 2 || at.row < s.rows) narrow_store<T>(dx + u * RPW * 2 * D, t, g);
+        }
     }
     // the ring's memory serves the sum over the block's warps once every warp is done with it
     sm100::cp_async_wait<0>();
@@ -628,30 +764,31 @@ __device__ __forceinline__ void gradient_rows(const Args &a, const Side &s, uint
     }
 }
 
-template <typename T, int D, bool SRC8>
+template <typename T, int D, bool SRC8, int U>
 __device__ __forceinline__ void gradient_side(const Args &a, const Side &s, uint32_t block,
-                                              uint32_t blocks, float *partial, void *smem) {
+                                              float *partial, void *smem) {
     if (s.norm == SLIKL_NORM_RMS)
-        gradient_rows<T, D, SLIKL_NORM_RMS, SRC8>(a, s, block, blocks, partial, smem);
+        gradient_rows<T, D, SLIKL_NORM_RMS, SRC8, U>(a, s, block, partial, smem);
     else if (s.norm == SLIKL_NORM_LAYER)
-        gradient_rows<T, D, SLIKL_NORM_LAYER, SRC8>(a, s, block, blocks, partial, smem);
+        gradient_rows<T, D, SLIKL_NORM_LAYER, SRC8, U>(a, s, block, partial, smem);
     else
-        gradient_rows<T, D, SLIKL_NORM_NONE, SRC8>(a, s, block, blocks, partial, smem);
+        gradient_rows<T, D, SLIKL_NORM_NONE, SRC8, U>(a, s, block, partial, smem);
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, 4) qk_gradient(const __grid_constant__ Args a) {
-    __shared__ __align__(16) unsigned char smem[sizeof(Ring<false, true>)];
-    static_assert(sizeof(Ring<true, true>) <= sizeof(smem), "ring of a checkpoint");
+__global__ void __launch_bounds__(kThreads, kGradPerSm) qk_gradient(const __grid_constant__ Args a) {
+    __shared__ __align__(16) unsigned char smem[kRingBytes<true>];
     const bool k = blockIdx.x >= a.blocks_q;
     const Side &s = a.side[k];
     const uint32_t block = blockIdx.x - (k ? a.blocks_q : 0);
-    const uint32_t blocks = k ? a.blocks_k : a.blocks_q;
     float *partial = a.partial + (k ? 2 * kGradBlocks * D : 0);
-    if (s.x || s.norm == SLIKL_NORM_NONE)
-        gradient_side<T, D, false>(a, s, block, blocks, partial, smem);
-    else
-        gradient_side<T, D, true>(a, s, block, blocks, partial, smem);
+    if (s.x || s.norm == SLIKL_NORM_NONE) {
+        if (s.two) gradient_side<T, D, false, 2>(a, s, block, partial, smem);
+        else gradient_side<T, D, false, 1>(a, s, block, partial, smem);
+    } else {
+        if (s.two) gradient_side<T, D, true, 2>(a, s, block, partial, smem);
+        else gradient_side<T, D, true, 1>(a, s, block, partial, smem);
+    }
 }
 
 struct Sums {
@@ -786,36 +923,52 @@ Args make_args(const slikl_qk_problem *p, const slikl_qk_tensors *t) {
     return a;
 }
 
-bool on_sm100() {
-    int dev = 0, major = 0;
-    return cudaGetDevice(&dev) == cudaSuccess &&
-           cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) == cudaSuccess &&
-           major == 10;
+// Multiprocessors of the current device; 0 where it cannot run these kernels.
+int sm100_multiprocessors() {
+    int dev = 0, major = 0, sms = 0;
+    const bool ok =
+        cudaGetDevice(&dev) == cudaSuccess &&
+        cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) == cudaSuccess &&
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess;
+    return ok && major == 10 ? sms : 0;
 }
 
-// Blocks of both sides, `most` at most, in proportion to the bytes they move (`each` for an element,
-// the angles for a token); a side with rows gets one at least. A small call gets a group of rows for
-// each warp, so that it spreads over all multiprocessors.
-void share_blocks(Args &a, int64_t D, uint32_t most, int each) {
-    const uint32_t tile = (uint32_t)(kThreads / 32) * (uint32_t)(512 / D);
-    uint32_t tiles[2];
-    double bytes[2];
+// Blocks of both sides, `most` at most, in proportion to the instructions that their rows take; a
+// side with rows gets one at least. (Counted on B200: a row of a token with few heads takes 1.6 times
+// as many as one of 64 heads, whose angles are ready, a layer norm 1.25 times an RMS norm's.) A
+// small call gets a group of rows for each warp, so that it spreads over all multiprocessors.
+void share_blocks(Args &a, int64_t D, int sms, int per_sm) {
+    const uint32_t most = (uint32_t)(std::min(sms, kMaxSms) * per_sm), warps = kThreads / 32;
+    const uint32_t rpw = (uint32_t)(512 / D);
+    uint32_t groups[2], blocks[2];
+    double cost[2];
     for (int i = 0; i < 2; ++i) {
-        const Side &s = a.side[i];
-        tiles[i] = (s.rows + tile - 1) / tile;
-        bytes[i] = (double)s.rows * ((double)each * D + 4.0 * a.rot / s.N.d);
+        Side &s = a.side[i];
+        // two rows a thread where a token's heads allow it and every warp still gets a group
+        s.two = s.N.d % (2 * rpw) == 0 && s.rows >= 2 * rpw * warps * most;
+        const uint32_t per = rpw << s.two;
+        groups[i] = (s.rows + per - 1) / per;
+        blocks[i] = (groups[i] + warps - 1) / warps;
+        cost[i] = s.rows * (1.0 + 0.6 / s.N.d) * (s.norm == SLIKL_NORM_LAYER ? 1.25 : 1.0);
     }
-    a.blocks_q = tiles[0];
-    a.blocks_k = tiles[1];
-    if ((uint64_t)tiles[0] + tiles[1] <= most) return;
-    const uint32_t share = (uint32_t)(most * (bytes[1] / (bytes[0] + bytes[1])) + 0.5);
-    a.blocks_k = tiles[1] == 0 ? 0 : std::min(tiles[1], std::max(share, 1u));
-    a.blocks_q = std::min(tiles[0], most - a.blocks_k);
+    if ((uint64_t)blocks[0] + blocks[1] > most) {
+        const uint32_t share = (uint32_t)(most * (cost[1] / (cost[0] + cost[1])) + 0.5);
+        blocks[1] = blocks[1] == 0 ? 0 : std::min(blocks[1], std::max(share, 1u));
+        blocks[0] = std::min(blocks[0], most - blocks[1]);
+    }
+    for (int i = 0; i < 2; ++i)
+        if (blocks[i]) {
+            a.side[i].per_warp = groups[i] / (blocks[i] * warps);
+            a.side[i].longer = groups[i] % (blocks[i] * warps);
+        }
+    a.blocks_q = blocks[0];
+    a.blocks_k = blocks[1];
 }
 
-slikl_status run_forward(const slikl_qk_problem *p, const slikl_qk_tensors *t, cudaStream_t st) {
+slikl_status run_forward(const slikl_qk_problem *p, const slikl_qk_tensors *t, int sms,
+                         cudaStream_t st) {
     Args a = make_args(p, t);
-    share_blocks(a, p->D, 5 * 148, 4);
+    share_blocks(a, p->D, sms, kFwdPerSm);
     const uint32_t blocks = a.blocks_q + a.blocks_k;
     if (blocks == 0) return SLIKL_OK;
     auto kernel = p->dtype == SLIKL_BF16
@@ -826,10 +979,10 @@ slikl_status run_forward(const slikl_qk_problem *p, const slikl_qk_tensors *t, c
 }
 
 slikl_status run_gradient(const slikl_qk_problem *p, const slikl_qk_tensors *t, float *partial,
-                          cudaStream_t st) {
+                          int sms, cudaStream_t st) {
     Args a = make_args(p, t);
     a.partial = partial;
-    share_blocks(a, p->D, 4 * 148, 6);
+    share_blocks(a, p->D, sms, kGradPerSm);
     if (a.blocks_q + a.blocks_k > 0) {
         auto kernel =
             p->dtype == SLIKL_BF16
@@ -893,8 +1046,9 @@ slikl_status slikl_qk_norm_rope(const slikl_qk_problem *problem, const slikl_qk_
     if (st != SLIKL_OK) return st;
     st = check_tensors(problem, tensors, false);
     if (st != SLIKL_OK) return st;
-    if (!on_sm100()) return SLIKL_ERR_CUDA;
-    return run_forward(problem, tensors, static_cast<cudaStream_t>(stream));
+    const int sms = sm100_multiprocessors();
+    if (!sms) return SLIKL_ERR_CUDA;
+    return run_forward(problem, tensors, sms, static_cast<cudaStream_t>(stream));
 }
 
 slikl_status slikl_qk_norm_rope_grad_workspace_size(const slikl_qk_problem *problem,
@@ -916,8 +1070,9 @@ slikl_status slikl_qk_norm_rope_grad(const slikl_qk_problem *problem,
     if (!workspace) return SLIKL_ERR_PARAM_NULLPTR;
     if (misaligned(workspace, 256)) return SLIKL_ERR_PARAM_INVALID;
     if (workspace_bytes < grad_workspace(problem)) return SLIKL_ERR_WORKSPACE_TOO_SMALL;
-    if (!on_sm100()) return SLIKL_ERR_CUDA;
-    return run_gradient(problem, tensors, static_cast<float *>(workspace),
+    const int sms = sm100_multiprocessors();
+    if (!sms) return SLIKL_ERR_CUDA;
+    return run_gradient(problem, tensors, static_cast<float *>(workspace), sms,
                         static_cast<cudaStream_t>(stream));
 }
 
@@ -965,14 +1120,15 @@ slikl_status slikl_grad_projected(const slikl_problem *problem, const slikl_qk_p
     // slikl_grad_ex's own checks, before this call's first launch
     st = check_index_call(problem, &tn, options, true);
     if (st != SLIKL_OK) return st;
-    if (!on_sm100()) return SLIKL_ERR_CUDA;
+    const int sms = sm100_multiprocessors();
+    if (!sms) return SLIKL_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    st = run_forward(qk, &qt, s);
+    st = run_forward(qk, &qt, sms, s);
     if (st != SLIKL_OK) return st;
     st = slikl_grad_ex(problem, &tn, workspace, L.q, stream, options);
     if (st != SLIKL_OK) return st;
     qt.status = reinterpret_cast<uint32_t *>(workspace);
-    return run_gradient(qk, &qt, reinterpret_cast<float *>(ws + L.partial), s);
+    return run_gradient(qk, &qt, reinterpret_cast<float *>(ws + L.partial), sms, s);
 }
 
 }  // extern "C"
