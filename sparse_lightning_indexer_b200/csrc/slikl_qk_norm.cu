@@ -73,7 +73,7 @@ struct Args {
     Side side[2];             // q, k
     uint32_t blocks_q;        // blocks of the q side; the others are the k side's
     uint32_t blocks_k;
-    int rot, pairs;           // rotated dims; neighbours (1) or halves (0)
+    int rot;                  // rotated dims
     uint32_t table_rows;
     float eps;
     const float *cos_sin;
@@ -82,7 +82,7 @@ struct Args {
 };
 
 constexpr int kThreads = 128;
-constexpr int kFwdPerSm = 6, kGradPerSm = 4;   // blocks that a multiprocessor's registers hold
+constexpr int kFwdPerSm = 6, kGradPerSm = 3;   // blocks that a multiprocessor's registers hold
 constexpr int kMaxSms = 256;
 constexpr int kGradBlocks = kMaxSms * kGradPerSm;   // most blocks of the gradient kernel (the
                                                     // workspace's size)
@@ -95,14 +95,15 @@ struct Lane {
     bool turns;               // rotated dims
 };
 
-__device__ __forceinline__ Lane lane_of(int l, int rot, int pairs, int D) {
+template <bool PAIRS>
+__device__ __forceinline__ Lane lane_of(int l, int rot, int D) {
     Lane t;
     const int half = rot / 16;
     t.turns = l < half;
     t.ca = t.turns ? 8 * l : rot + 8 * (l - half);
     t.cb = t.ca + (t.turns ? rot : D - rot) / 2;
-    t.ta = pairs ? 4 * l : 8 * l;
-    t.tb = pairs ? 4 * l + rot / 4 : t.ta + 4;
+    t.ta = PAIRS ? 4 * l : 8 * l;
+    t.tb = PAIRS ? 4 * l + rot / 4 : t.ta + 4;
     return t;
 }
 
@@ -133,8 +134,31 @@ __device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
 }
 __device__ __forceinline__ float both(Pair a) { return a.f.x + a.f.y; }
 
-// The thread's 16 values as pairs of neighbours: [0, 4) its first chunk, [4, 8) its second.
-// c, s: cosines and sines of its 8 angles.
+// The thread's 16 values as eight pairs, v[i] meeting v[i + 4] in the rotation for i < 4. Halves: v
+// holds neighbours, the first chunk's in [0, 4) and the second's in [4, 8). PAIRS: word p of the two
+// chunks (eight words of two 16-bit values) holds the two values that angle p turns; the low ones of
+// words 2i and 2i + 1 are v[i], the high ones v[i + 4]. So both layouts are turned by the same
+// code, and differ in where a value comes from alone.
+template <bool PAIRS>
+__device__ __forceinline__ float2 word(const Pair *v, int p) {
+    if (!PAIRS) return v[p].f;
+    return p & 1 ? make_float2(v[p / 2].f.y, v[p / 2 + 4].f.y)
+                 : make_float2(v[p / 2].f.x, v[p / 2 + 4].f.x);
+}
+template <bool PAIRS>
+__device__ __forceinline__ void set_word(Pair *v, int p, float2 f) {
+    if (!PAIRS) {
+        v[p].f = f;
+    } else if (p & 1) {
+        v[p / 2].f.y = f.x;
+        v[p / 2 + 4].f.y = f.y;
+    } else {
+        v[p / 2].f.x = f.x;
+        v[p / 2 + 4].f.x = f.y;
+    }
+}
+
+// Cosines and sines of the thread's eight angles: c[i], s[i] belong to v[i] and v[i + 4].
 struct Angles {
     Pair c[4], s[4];
 };
@@ -157,97 +181,73 @@ struct Turner {
     Pair c[8], s[8];
 };
 
-__device__ __forceinline__ Pair swapped(Pair p) { return pair(p.f.y, p.f.x); }
-
 __device__ __forceinline__ void form_turner(const Args &a, const Lane &t, const Pair *gain,
                                             int32_t pos, Turner &o) {
     Angles g;
 #pragma unroll
     for (int i = 0; i < 4; ++i) g.c[i] = pair(1.f, 1.f), g.s[i] = pair(0.f, 0.f);
     if (t.turns) load_angles(a, t, pos, g);
-    if (a.pairs) {
+    const Pair minus = pair(-1.f, -1.f);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float c = i & 1 ? g.c[i / 2].f.y : g.c[i / 2].f.x;
-            const float s = i & 1 ? g.s[i / 2].f.y : g.s[i / 2].f.x;
-            o.c[i] = gain[i] * pair(c, c);
-            o.s[i] = swapped(gain[i]) * pair(-s, s);
-        }
-    } else {
-        const Pair minus = pair(-1.f, -1.f);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            o.c[i] = gain[i] * g.c[i];
-            o.c[i + 4] = gain[i + 4] * g.c[i];
-            o.s[i] = gain[i + 4] * g.s[i] * minus;
-            o.s[i + 4] = gain[i] * g.s[i];
-        }
+    for (int i = 0; i < 4; ++i) {
+        o.c[i] = gain[i] * g.c[i];
+        o.c[i + 4] = gain[i + 4] * g.c[i];
+        o.s[i] = gain[i + 4] * g.s[i] * minus;
+        o.s[i + 4] = gain[i] * g.s[i];
     }
 }
 
-__device__ __forceinline__ void turn(Pair *v, const Turner &o, int pairs) {
-    if (pairs) {
+__device__ __forceinline__ void turn(Pair *v, const Turner &o) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = fma2(v[i], o.c[i], swapped(v[i]) * o.s[i]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const Pair x = v[i], y = v[i + 4];
-            v[i] = fma2(x, o.c[i], y * o.s[i]);
-            v[i + 4] = fma2(y, o.c[i + 4], x * o.s[i + 4]);
-        }
+    for (int i = 0; i < 4; ++i) {
+        const Pair x = v[i], y = v[i + 4];
+        v[i] = fma2(x, o.c[i], y * o.s[i]);
+        v[i + 4] = fma2(y, o.c[i + 4], x * o.s[i + 4]);
     }
 }
 
-// Turns the values by the angles, or (BACK) by minus the angles. Halves: pairs of angles meet pairs
-// of values. Pairs: the angle of v[i] is half i & 1 of angle pair i / 2.
+// Turns the values by the angles, or (BACK) by minus the angles.
 template <bool BACK>
-__device__ __forceinline__ void turn(Pair *v, const Angles &g, int pairs) {
-    if (pairs) {
+__device__ __forceinline__ void turn(Pair *v, const Angles &g) {
+    const Pair minus = pair(-1.f, -1.f);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float c = i & 1 ? g.c[i / 2].f.y : g.c[i / 2].f.x;
-            const float s0 = i & 1 ? g.s[i / 2].f.y : g.s[i / 2].f.x, s = BACK ? -s0 : s0;
-            const float x = v[i].f.x, y = v[i].f.y;
-            v[i].f.x = fmaf(x, c, -(y * s));
-            v[i].f.y = fmaf(y, c, x * s);
-        }
-    } else {
-        const Pair minus = pair(-1.f, -1.f);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const Pair x = v[i], y = v[i + 4], xs = x * g.s[i], ys = y * g.s[i];
-            v[i] = fma2(x, g.c[i], BACK ? ys : ys * minus);
-            v[i + 4] = fma2(y, g.c[i], BACK ? xs * minus : xs);
-        }
+    for (int i = 0; i < 4; ++i) {
+        const Pair x = v[i], y = v[i + 4], xs = x * g.s[i], ys = y * g.s[i];
+        v[i] = fma2(x, g.c[i], BACK ? ys : ys * minus);
+        v[i + 4] = fma2(y, g.c[i], BACK ? xs * minus : xs);
     }
 }
 
-template <typename T>
+template <typename T, bool PAIRS>
 __device__ __forceinline__ void widen(const uint4 &a, const uint4 &b, Pair *v) {
     const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i].f = unpack2<T>(w[i]);
+    for (int p = 0; p < 8; ++p) set_word<PAIRS>(v, p, unpack2<T>(w[p]));
 }
 
+template <bool PAIRS>
 __device__ __forceinline__ void widen8(const uint2 &a, const uint2 &b, float scale, Pair *v) {
     const uint32_t w[4] = {a.x, a.y, b.x, b.y};
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+        const __nv_fp8x2_storage_t two = (__nv_fp8x2_storage_t)(w[p >> 1] >> (16 * (p & 1)));
+        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(two, __NV_E4M3);
+        set_word<PAIRS>(v, p, __half22float2(__half2(h)));
+    }
     const Pair s = pair(scale, scale);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const __nv_fp8x2_storage_t two = (__nv_fp8x2_storage_t)(w[i >> 1] >> (16 * (i & 1)));
-        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(two, __NV_E4M3);
-        v[i].f = __half22float2(__half2(h));
-        v[i] = v[i] * s;
-    }
+    for (int i = 0; i < 8; ++i) v[i] = v[i] * s;
 }
 
 // Stores the thread's 16 values as 16-bit ones; `first`: where its first chunk goes.
-template <typename T>
+template <typename T, bool PAIRS>
 __device__ __forceinline__ void narrow_store(char *first, const Lane &t, const Pair *v) {
     uint32_t w[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = pack2<T>(v[i].f.x, v[i].f.y);
+    for (int p = 0; p < 8; ++p) {
+        const float2 f = word<PAIRS>(v, p);
+        w[p] = pack2<T>(f.x, f.y);
+    }
     *reinterpret_cast<uint4 *>(first) = make_uint4(w[0], w[1], w[2], w[3]);
     *reinterpret_cast<uint4 *>(first + 2 * (t.cb - t.ca)) = make_uint4(w[4], w[5], w[6], w[7]);
 }
@@ -459,21 +459,25 @@ struct Fetch {
     }
 };
 
-template <typename T, bool SRC8, bool GRAD, int U>
+template <typename T, bool PAIRS, bool SRC8, bool GRAD, int U>
 __device__ __forceinline__ void source(const Stage<SRC8, GRAD, U> &from, int u, Pair *v) {
     const int i = threadIdx.x;
     const uint4 x = from.x[u][0][i];
-    if (SRC8) widen8(make_uint2(x.x, x.y), make_uint2(x.z, x.w), from.scale[SRC8 ? u : 0][SRC8 ? i : 0], v);
-    else widen<T>(x, from.x[u][SRC8 ? 0 : 1][i], v);
+    if (SRC8) widen8<PAIRS>(make_uint2(x.x, x.y), make_uint2(x.z, x.w), from.scale[SRC8 ? u : 0][SRC8 ? i : 0], v);
+    else widen<T, PAIRS>(x, from.x[u][SRC8 ? 0 : 1][i], v);
 }
 
+// The thread's 16 of D fp32 values (a gain or a bias).
+template <bool PAIRS>
 __device__ __forceinline__ void load16(const float *p, const Lane &t, Pair *v) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const float4 *q = reinterpret_cast<const float4 *>(p + (h ? t.cb : t.ca));
         const float4 u = q[0], w = q[1];
-        v[4 * h] = pair(u.x, u.y), v[4 * h + 1] = pair(u.z, u.w);
-        v[4 * h + 2] = pair(w.x, w.y), v[4 * h + 3] = pair(w.z, w.w);
+        set_word<PAIRS>(v, 4 * h, make_float2(u.x, u.y));
+        set_word<PAIRS>(v, 4 * h + 1, make_float2(u.z, u.w));
+        set_word<PAIRS>(v, 4 * h + 2, make_float2(w.x, w.y));
+        set_word<PAIRS>(v, 4 * h + 3, make_float2(w.z, w.w));
     }
 }
 
@@ -501,7 +505,7 @@ __device__ __forceinline__ uint32_t top_of<__half>(const uint4 &a, const uint4 &
 // reciprocals: the scale may be off by its last bit, and a value halfway between two codes may
 // round the other way. Every lane of the warp has to come here (the maximum crosses lanes); rows
 // that are not `in` are not stored. `top`: top_of the thread's values.
-template <typename T, int D>
+template <typename T, int D, bool PAIRS>
 __device__ __forceinline__ void keep_row(const Side &s, uint32_t row, const Lane &t, int l,
                                          bool in, uint32_t top, const Pair *x) {
     const float2 two = unpack2<T>(top);
@@ -511,11 +515,14 @@ __device__ __forceinline__ void keep_row(const Side &s, uint32_t row, const Lane
     const float scale = m > 0.f ? fmaxf(m * (1.f / 448.f), FLT_MIN) : 0.f;
     const float inv = m > 0.f ? __fdividef(1.f, scale) : 0.f;
     const Pair by = pair(inv, inv);
+    Pair q[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = x[i] * by;
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t lo = __nv_cvt_float2_to_fp8x2((x[2 * i] * by).f, __NV_SATFINITE, __NV_E4M3);
-        const uint32_t hi = __nv_cvt_float2_to_fp8x2((x[2 * i + 1] * by).f, __NV_SATFINITE, __NV_E4M3);
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(word<PAIRS>(q, 2 * i), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi = __nv_cvt_float2_to_fp8x2(word<PAIRS>(q, 2 * i + 1), __NV_SATFINITE, __NV_E4M3);
         w[i] = __byte_perm(lo, hi, 0x5410);
     }
     uint8_t *p = s.keep8 + t.ca + (uint64_t)row * D;
@@ -524,13 +531,13 @@ __device__ __forceinline__ void keep_row(const Side &s, uint32_t row, const Lane
     if (l == 0) s.keep8_scale[row] = scale;
 }
 
-template <typename T, int D, int NORM, bool SRC8, int U>
+template <typename T, int D, bool PAIRS, int NORM, bool SRC8, int U>
 __device__ __forceinline__ void forward_rows(const Args &a, const Side &s, uint32_t block,
                                              void *smem) {
     constexpr int TPR = D / 16, RPW = 32 / TPR;
     auto &ring = *static_cast<Ring<SRC8, false, U> *>(smem);
     const int l = (threadIdx.x & 31) % TPR;
-    const Lane t = lane_of(l, a.rot, a.pairs, D);
+    const Lane t = lane_of<PAIRS>(l, a.rot, D);
     const Walk<RPW, U> walk(s, block, (threadIdx.x & 31) / TPR);
     const int32_t steps = walk.steps;
     uint32_t row = walk.row, stage = 0;
@@ -563,7 +570,7 @@ __device__ __forceinline__ void forward_rows(const Args &a, const Side &s, uint3
                 Pair gain[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) gain[j] = pair(1.f, 1.f);
-                if (s.gain) load16(s.gain, t, gain);
+                if (s.gain) load16<PAIRS>(s.gain, t, gain);
                 form_turner(a, t, gain, pos, turner);
             }
         }
@@ -574,9 +581,9 @@ __device__ __forceinline__ void forward_rows(const Args &a, const Side &s, uint3
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             Pair v[8];
-            source<T>(now, u, v);
+            source<T, PAIRS>(now, u, v);
             if (!SRC8 && s.keep8)
-                keep_row<T, D>(s, row + u * RPW, t, l, in,
+                keep_row<T, D, PAIRS>(s, row + u * RPW, t, l, in,
                                top_of<T>(now.x[u][0][threadIdx.x], now.x[u][SRC8 ? 0 : 1][threadIdx.x]), v);
             if (!s.y) continue;
             if (NORM != SLIKL_NORM_NONE) {
@@ -593,64 +600,64 @@ __device__ __forceinline__ void forward_rows(const Args &a, const Side &s, uint3
                 }
                 if (s.gain) {
                     Pair gain[8];
-                    load16(s.gain, t, gain);
+                    load16<PAIRS>(s.gain, t, gain);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) v[j] = v[j] * gain[j];
                 }
                 if (s.bias) {
                     Pair bias[8];
-                    load16(s.bias, t, bias);
+                    load16<PAIRS>(s.bias, t, bias);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) v[j] = v[j] + bias[j];
                 }
-                if (t.turns) turn<false>(v, angles, a.pairs);
+                if (t.turns) turn<false>(v, angles);
             } else if (NORM != SLIKL_NORM_NONE || a.rot) {
-                turn(v, turner, a.pairs);
+                turn(v, turner);
             }
-            narrow_store<T>(y + u * RPW * 2 * D, t, v);
+            narrow_store<T, PAIRS>(y + u * RPW * 2 * D, t, v);
         }
     }
 }
 
-template <typename T, int D, bool SRC8, int U>
+template <typename T, int D, bool PAIRS, bool SRC8, int U>
 __device__ __forceinline__ void forward_side(const Args &a, const Side &s, uint32_t block,
                                              void *smem) {
     if (s.norm == SLIKL_NORM_RMS)
-        forward_rows<T, D, SLIKL_NORM_RMS, SRC8, U>(a, s, block, smem);
+        forward_rows<T, D, PAIRS, SLIKL_NORM_RMS, SRC8, U>(a, s, block, smem);
     else if (s.norm == SLIKL_NORM_LAYER)
-        forward_rows<T, D, SLIKL_NORM_LAYER, SRC8, U>(a, s, block, smem);
+        forward_rows<T, D, PAIRS, SLIKL_NORM_LAYER, SRC8, U>(a, s, block, smem);
     else
-        forward_rows<T, D, SLIKL_NORM_NONE, SRC8, U>(a, s, block, smem);
+        forward_rows<T, D, PAIRS, SLIKL_NORM_NONE, SRC8, U>(a, s, block, smem);
 }
 
-template <typename T, int D>
+template <typename T, int D, bool PAIRS>
 __global__ void __launch_bounds__(kThreads, kFwdPerSm) qk_forward(const __grid_constant__ Args a) {
     __shared__ __align__(16) unsigned char smem[kRingBytes<false>];
     const bool k = blockIdx.x >= a.blocks_q;
     const Side &s = a.side[k];
     const uint32_t block = blockIdx.x - (k ? a.blocks_q : 0);
     if (s.x) {
-        if (s.two) forward_side<T, D, false, 2>(a, s, block, smem);
-        else forward_side<T, D, false, 1>(a, s, block, smem);
+        if (s.two) forward_side<T, D, PAIRS, false, 2>(a, s, block, smem);
+        else forward_side<T, D, PAIRS, false, 1>(a, s, block, smem);
     } else {
-        if (s.two) forward_side<T, D, true, 2>(a, s, block, smem);
-        else forward_side<T, D, true, 1>(a, s, block, smem);
+        if (s.two) forward_side<T, D, PAIRS, true, 2>(a, s, block, smem);
+        else forward_side<T, D, PAIRS, true, 1>(a, s, block, smem);
     }
 }
 
 // Gradient: the sums of dgain and dbias stay in registers over a warp's rows, are added over the
 // block in a fixed order and stored; qk_grad_sums adds the blocks' sums, again in a fixed order.
 // With x less its mean, h = dz gain:
-//   dbias += dz,  dgain += dz (x r),  dx = r (h - [mean(h)]) - (x r) r^2 mean(h x)
-template <typename T, int D, int NORM, bool SRC8, int U>
+//   dbias += dz,  dgain += (dz x) r,  dx = r (h - [mean(h)]) - x r^3 mean(h x)
+template <typename T, int D, bool PAIRS, int NORM, bool SRC8, int U>
 __device__ __forceinline__ void gradient_rows(const Args &a, const Side &s, uint32_t block,
-                                              float *partial, void *ring_smem) {
+                                              float *partial, void *ring_smem, float4 *gains) {
     constexpr int TPR = D / 16, RPW = 32 / TPR, WARPS = kThreads / 32;
     constexpr bool X = NORM != SLIKL_NORM_NONE;        // without a norm x is not needed
     constexpr bool LAYER = NORM == SLIKL_NORM_LAYER;
     auto &ring = *static_cast<Ring<SRC8, true, U> *>(ring_smem);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const Lane t = lane_of(lane % TPR, a.rot, a.pairs, D);
+    const Lane t = lane_of<PAIRS>(lane % TPR, a.rot, D);
     Walk<RPW, U> at(s, block, lane / TPR);
     const int32_t steps = at.steps;
     uint32_t stage = 0;
@@ -660,16 +667,26 @@ __device__ __forceinline__ void gradient_rows(const Args &a, const Side &s, uint
         if (i < steps) fetch.next(ring, a, s, t);
         else cp_async_commit();
     }
-    Pair gain[8], dgain[8], dbias[8];
+    // the thread's gains, as its four 16-byte pieces in a row with the other threads' same pieces:
+    // registers are short here, and every row reads each gain once
+    if (X && threadIdx.x < TPR) {
+        Pair gain[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) gain[j] = pair(1.f, 1.f);
+        if (s.gain) load16<PAIRS>(s.gain, t, gain);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            gains[j * TPR + threadIdx.x] =
+                make_float4(gain[2 * j].f.x, gain[2 * j].f.y, gain[2 * j + 1].f.x, gain[2 * j + 1].f.y);
+    }
+    __syncthreads();
+    Pair dgain[8], dbias[8];
     Angles angles;
     int32_t turned_to = -1;
 #pragma unroll
     for (int i = 0; i < 4; ++i) angles.c[i] = angles.s[i] = pair(0.f, 0.f);
-    if (X) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) gain[i] = pair(1.f, 1.f), dgain[i] = dbias[i] = pair(0.f, 0.f);
-        if (s.gain) load16(s.gain, t, gain);
-    }
+    for (int i = 0; i < 8; ++i) dgain[i] = dbias[i] = pair(0.f, 0.f);
     for (int32_t i = 0; i < steps; ++i, at.step(s)) {
         sm100::cp_async_wait<kStages<true, U> - 2>();
         const auto &now = ring[stage];
@@ -683,49 +700,59 @@ __device__ __forceinline__ void gradient_rows(const Args &a, const Side &s, uint
         else cp_async_commit();
         char *dx = static_cast<char *>(s.dx) + 2 * t.ca + (uint64_t)at.token * s.dx_stride +
                    at.head * (2 * D);
-#pragma unroll 1
-        for (int u = 0; u < U; ++u) {      // (two rows at once would not fit the registers)
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
             Pair g[8], v[8];
-            widen<T>(now.dy[u][0][threadIdx.x], now.dy[u][1][threadIdx.x], g);
-            if (X) source<T>(now, u, v);
-            if (t.turns) turn<true>(g, angles, a.pairs);
+            widen<T, PAIRS>(now.dy[u][0][threadIdx.x], now.dy[u][1][threadIdx.x], g);
+            if (X) source<T, PAIRS>(now, u, v);
+            if (t.turns) turn<true>(g, angles);
             if (X) {
                 // two rounds of sums over the row's threads, each of two sums side by side: the means
                 // of x and h (layer only), then x^2 and h x
                 float lift = 0.f;
+                Pair e[8];
                 if (LAYER) {
-                    Pair sum = g[0] * gain[0];
+                    const float m = both(sum8(v));
+                    float sx = m, sh;
+                    Pair sum = pair(0.f, 0.f);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        if (j) sum = fma2(g[j], gain[j], sum);
-                        dbias[j] = dbias[j] + g[j];
+                    for (int j = 0; j < 4; ++j) {
+                        const float4 w = gains[j * TPR + lane % TPR];
+                        sum = fma2(g[2 * j], pair(w.x, w.y), sum);
+                        sum = fma2(g[2 * j + 1], pair(w.z, w.w), sum);
                     }
-                    float sx = both(sum8(v)), sh = both(sum);
+                    sh = both(sum);
                     row_sums<TPR>(sx, sh);
                     lift = sh * (-1.f / D);
                     const Pair less = pair(sx * (-1.f / D), sx * (-1.f / D));
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) v[j] = v[j] + less;
+                    for (int j = 0; j < 8; ++j) {
+                        v[j] = v[j] + less;
+                        dbias[j] = dbias[j] + g[j];
+                    }
                 }
-                Pair sum = (g[0] * gain[0]) * v[0], more = (g[1] * gain[1]) * v[1];
+                Pair sum = pair(0.f, 0.f), more = sum;
 #pragma unroll
-                for (int j = 2; j < 8; j += 2) {
-                    sum = fma2(g[j] * gain[j], v[j], sum);
-                    more = fma2(g[j + 1] * gain[j + 1], v[j + 1], more);
+                for (int j = 0; j < 4; ++j) {
+                    const float4 w = gains[j * TPR + lane % TPR];
+                    e[2 * j] = g[2 * j] * v[2 * j];
+                    e[2 * j + 1] = g[2 * j + 1] * v[2 * j + 1];
+                    sum = fma2(e[2 * j], pair(w.x, w.y), sum);
+                    more = fma2(e[2 * j + 1], pair(w.z, w.w), more);
+                    g[2 * j] = g[2 * j] * pair(w.x, w.y);            // h from here on
+                    g[2 * j + 1] = g[2 * j + 1] * pair(w.z, w.w);
                 }
                 float sq = both(dot8(v, v)), sh = both(sum + more);
                 row_sums<TPR>(sq, sh);
-                const float r = rsqrtf(fmaf(sq, 1.f / D, a.eps)), m = sh * (r * r * (-1.f / D));
-                const Pair by = pair(r, r), along = pair(m, m), up = pair(lift, lift);
+                const float r = rsqrtf(fmaf(sq, 1.f / D, a.eps)), m = sh * (r * r * r * (-1.f / D));
+                const Pair by = pair(r, r), along = pair(m, m), up = pair(r * lift, r * lift);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    v[j] = v[j] * by;
-                    dgain[j] = fma2(g[j], v[j], dgain[j]);
-                    const Pair h = LAYER ? fma2(g[j], gain[j], up) : g[j] * gain[j];
-                    g[j] = fma2(h, by, v[j] * along);
+                    dgain[j] = fma2(e[j], by, dgain[j]);
+                    g[j] = fma2(v[j], along, LAYER ? fma2(g[j], by, up) : g[j] * by);
                 }
             }
-            if (U == 2 || at.row < s.rows) narrow_store<T>(dx + u * RPW * 2 * D, t, g);
+            if (U == 2 || at.row < s.rows) narrow_store<T, PAIRS>(dx + u * RPW * 2 * D, t, g);
         }
     }
     // the ring's memory serves the sum over the block's warps once every warp is done with it
@@ -735,11 +762,12 @@ __device__ __forceinline__ void gradient_rows(const Args &a, const Side &s, uint
     if constexpr (NORM != SLIKL_NORM_NONE) {
 #pragma unroll
         for (int which = 0; which < (NORM == SLIKL_NORM_LAYER ? 2 : 1); ++which) {
-            float acc[16];
+            float acc[16];                // by the values' places in the two chunks
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                acc[2 * i] = which ? dbias[i].f.x : dgain[i].f.x;
-                acc[2 * i + 1] = which ? dbias[i].f.y : dgain[i].f.y;
+            for (int p = 0; p < 8; ++p) {
+                const float2 f = word<PAIRS>(which ? dbias : dgain, p);
+                acc[2 * p] = f.x;
+                acc[2 * p + 1] = f.y;
             }
 #pragma unroll
             for (int i = 0; i < 16; ++i)
@@ -764,30 +792,31 @@ __device__ __forceinline__ void gradient_rows(const Args &a, const Side &s, uint
     }
 }
 
-template <typename T, int D, bool SRC8, int U>
+template <typename T, int D, bool PAIRS, bool SRC8, int U>
 __device__ __forceinline__ void gradient_side(const Args &a, const Side &s, uint32_t block,
-                                              float *partial, void *smem) {
+                                              float *partial, void *smem, float4 *gains) {
     if (s.norm == SLIKL_NORM_RMS)
-        gradient_rows<T, D, SLIKL_NORM_RMS, SRC8, U>(a, s, block, partial, smem);
+        gradient_rows<T, D, PAIRS, SLIKL_NORM_RMS, SRC8, U>(a, s, block, partial, smem, gains);
     else if (s.norm == SLIKL_NORM_LAYER)
-        gradient_rows<T, D, SLIKL_NORM_LAYER, SRC8, U>(a, s, block, partial, smem);
+        gradient_rows<T, D, PAIRS, SLIKL_NORM_LAYER, SRC8, U>(a, s, block, partial, smem, gains);
     else
-        gradient_rows<T, D, SLIKL_NORM_NONE, SRC8, U>(a, s, block, partial, smem);
+        gradient_rows<T, D, PAIRS, SLIKL_NORM_NONE, SRC8, U>(a, s, block, partial, smem, gains);
 }
 
-template <typename T, int D>
+template <typename T, int D, bool PAIRS>
 __global__ void __launch_bounds__(kThreads, kGradPerSm) qk_gradient(const __grid_constant__ Args a) {
     __shared__ __align__(16) unsigned char smem[kRingBytes<true>];
+    __shared__ float4 gains[D / 4];
     const bool k = blockIdx.x >= a.blocks_q;
     const Side &s = a.side[k];
     const uint32_t block = blockIdx.x - (k ? a.blocks_q : 0);
     float *partial = a.partial + (k ? 2 * kGradBlocks * D : 0);
     if (s.x || s.norm == SLIKL_NORM_NONE) {
-        if (s.two) gradient_side<T, D, false, 2>(a, s, block, partial, smem);
-        else gradient_side<T, D, false, 1>(a, s, block, partial, smem);
+        if (s.two) gradient_side<T, D, PAIRS, false, 2>(a, s, block, partial, smem, gains);
+        else gradient_side<T, D, PAIRS, false, 1>(a, s, block, partial, smem, gains);
     } else {
-        if (s.two) gradient_side<T, D, true, 2>(a, s, block, partial, smem);
-        else gradient_side<T, D, true, 1>(a, s, block, partial, smem);
+        if (s.two) gradient_side<T, D, PAIRS, true, 2>(a, s, block, partial, smem, gains);
+        else gradient_side<T, D, PAIRS, true, 1>(a, s, block, partial, smem, gains);
     }
 }
 
@@ -803,9 +832,14 @@ __global__ void __launch_bounds__(1024) qk_grad_sums(Sums a) {
     __shared__ float smem[32][33];
     const int which = blockIdx.y, col = blockIdx.x * 32 + (threadIdx.x & 31), part = threadIdx.x >> 5;
     if (!a.out[which]) return;
-    float sum = 0.f;
-    for (uint32_t b = part; b < a.blocks[which]; b += 32)
-        sum += a.partial[((int64_t)which * kGradBlocks + b) * a.D + col];
+    // eight loads on the way at once: one after another they took 4 us
+    float sums[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    const float *from = a.partial + (int64_t)which * kGradBlocks * a.D + col;
+    for (uint32_t b = part; b < a.blocks[which]; b += 256)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (b + 32 * i < a.blocks[which]) sums[i] += from[(int64_t)(b + 32 * i) * a.D];
+    float sum = ((sums[0] + sums[1]) + (sums[2] + sums[3])) + ((sums[4] + sums[5]) + (sums[6] + sums[7]));
     smem[part][threadIdx.x & 31] = sum;
     __syncthreads();
     if (part == 0) {
@@ -915,7 +949,6 @@ Args make_args(const slikl_qk_problem *p, const slikl_qk_tensors *t) {
     a.side[0] = make_side(p, p->q, t->q);
     a.side[1] = make_side(p, p->k, t->k);
     a.rot = (int)p->rot_dim;
-    a.pairs = p->rot_layout == SLIKL_ROT_PAIRS;
     a.table_rows = (uint32_t)p->table_rows;
     a.eps = p->eps;
     a.cos_sin = t->cos_sin;
@@ -965,15 +998,33 @@ void share_blocks(Args &a, int64_t D, int sms, int per_sm) {
     a.blocks_k = blocks[1];
 }
 
+using Kernel = void (*)(Args);
+struct Forward {
+    template <typename T, int D, bool PAIRS>
+    Kernel get() const { return qk_forward<T, D, PAIRS>; }
+};
+struct Gradient {
+    template <typename T, int D, bool PAIRS>
+    Kernel get() const { return qk_gradient<T, D, PAIRS>; }
+};
+template <typename T, typename K>
+Kernel pick_of(const slikl_qk_problem &p, const K &k) {
+    const bool pairs = p.rot_layout == SLIKL_ROT_PAIRS;
+    if (p.D == 128) return pairs ? k.template get<T, 128, true>() : k.template get<T, 128, false>();
+    return pairs ? k.template get<T, 64, true>() : k.template get<T, 64, false>();
+}
+template <typename K>
+Kernel pick(const slikl_qk_problem &p, const K &k) {
+    return p.dtype == SLIKL_BF16 ? pick_of<__nv_bfloat16>(p, k) : pick_of<__half>(p, k);
+}
+
 slikl_status run_forward(const slikl_qk_problem *p, const slikl_qk_tensors *t, int sms,
                          cudaStream_t st) {
     Args a = make_args(p, t);
     share_blocks(a, p->D, sms, kFwdPerSm);
     const uint32_t blocks = a.blocks_q + a.blocks_k;
     if (blocks == 0) return SLIKL_OK;
-    auto kernel = p->dtype == SLIKL_BF16
-                      ? (p->D == 128 ? qk_forward<__nv_bfloat16, 128> : qk_forward<__nv_bfloat16, 64>)
-                      : (p->D == 128 ? qk_forward<__half, 128> : qk_forward<__half, 64>);
+    const auto kernel = pick(*p, Forward{});
     kernel<<<blocks, kThreads, 0, st>>>(a);
     return cudaGetLastError() == cudaSuccess ? SLIKL_OK : SLIKL_ERR_CUDA;
 }
@@ -984,10 +1035,7 @@ slikl_status run_gradient(const slikl_qk_problem *p, const slikl_qk_tensors *t, 
     a.partial = partial;
     share_blocks(a, p->D, sms, kGradPerSm);
     if (a.blocks_q + a.blocks_k > 0) {
-        auto kernel =
-            p->dtype == SLIKL_BF16
-                ? (p->D == 128 ? qk_gradient<__nv_bfloat16, 128> : qk_gradient<__nv_bfloat16, 64>)
-                : (p->D == 128 ? qk_gradient<__half, 128> : qk_gradient<__half, 64>);
+        const auto kernel = pick(*p, Gradient{});
         kernel<<<a.blocks_q + a.blocks_k, kThreads, 0, st>>>(a);
         if (cudaGetLastError() != cudaSuccess) return SLIKL_ERR_CUDA;
     }
