@@ -722,6 +722,23 @@ class Checkpoint(NamedTuple):
     dtype: torch.dtype
 
 
+_binding = None
+
+
+def _load_binding():
+    """The C++ marshalling of torch tensors (built by sparse_lightning_indexer_b200.build)."""
+    global _binding
+    if _binding is None:
+        load_library()
+        try:
+            from . import _slikl_torch
+        except ImportError as e:
+            raise RuntimeError("_slikl_torch.so is missing or does not fit this torch: "
+                               f"run python -m sparse_lightning_indexer_b200.build ({e})") from e
+        _binding = _slikl_torch
+    return _binding
+
+
 def _on_stream(f):
     """f with its `stream` argument, where one is given, as the current stream: what f allocates
     then belongs to that stream too."""
@@ -734,112 +751,13 @@ def _on_stream(f):
     return call
 
 
-def _launch(index, call, *args):
-    """call(*args, stream) on device `index` and its current stream."""
-    stream = torch._C._cuda_getCurrentRawStream(index)
-    if torch.cuda.current_device() == index:
-        call(*args, stream)
-    else:
-        with torch.cuda.device(index):
-            call(*args, stream)
-
-
-def _at(t, name, index, dtype, shape=None):
-    """Device address of a contiguous tensor of CUDA device `index`, this type and shape."""
-    if (t.get_device() != index or t.dtype is not dtype or not t.is_contiguous()
-            or (shape is not None and t.shape != shape)):
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor on cuda:{index}"
-                         + (f" of shape {tuple(shape)}" if shape is not None else "")
-                         + f", not {t.dtype} {tuple(t.shape)} on {t.device}")
-    return t.data_ptr()
-
-
-def _row_stride(t, name):
-    """Elements from one row to the next of t [B, S, N, D] or [T, N, D] whose heads are dense."""
-    shape = t.shape
-    dense = shape[-2] * shape[-1]
-    if t.is_contiguous():
-        return dense
-    st, row = t.stride(), dense
-    if st[-1] != 1 or (shape[-2] > 1 and st[-2] != shape[-1]):
-        raise ValueError(f"{name}: the heads of a row must be contiguous")
-    if len(shape) == 3:
-        if shape[0] > 1:
-            row = st[0]
-    elif shape[1] > 1:
-        row = st[1]
-        if shape[0] > 1 and st[0] != shape[1] * row:
-            raise ValueError(f"{name}: the batches must follow one another at the rows' stride")
-    elif shape[0] > 1:
-        row = st[0]
-    if row < dense or row % 8:
-        raise ValueError(f"{name}: row stride {row} is not a multiple of 8 of at least N*D = {dense}")
-    return row
-
-
-def _qk_side(side, tn, x, name, layout, index, D, dtype, rot, positions, gain, bias, norm):
-    """Enters one side, x or its Checkpoint, with what both directions read of it; returns its shape."""
-    if norm not in _NORMS or layout not in _LAYOUTS:
-        raise ValueError(f"norm_{name} must be one of {sorted(_NORMS)}, layout_{name} of {sorted(_LAYOUTS)}")
-    if type(x) is Checkpoint:
-        shape = x.values.shape
-        tn.x8 = _at(x.values, f"x_{name}.values", index, torch.float8_e4m3fn)
-        tn.x8_scale = _at(x.scale, f"x_{name}.scale", index, torch.float32, shape[:-1])
-    else:
-        shape = x.shape
-        if x.get_device() != index:
-            raise ValueError(f"x_{name} must be on cuda:{index}")
-        tn.x = x.data_ptr()
-    bsnd = layout == "BSND"
-    if len(shape) != (4 if bsnd else 3) or shape[-1] != D or x.dtype is not dtype:
-        raise ValueError("q and k must be BSND or TND rows that share D and one dtype, float16 or bfloat16")
-    if type(x) is not Checkpoint:
-        side.x_stride = _row_stride(x, f"x_{name}")
-    side.N, side.norm = shape[-2], _NORMS[norm]
-    side.T = T = shape[0] * shape[1] if bsnd else shape[0]
-    side.S = max(1, shape[1]) if bsnd else 1
-    if positions is not None:
-        tn.positions = _at(positions, f"pos_{name}", index, torch.int32)
-        if positions.numel() != T:
-            raise ValueError(f"pos_{name} must have {T} entries")
-    elif rot and T and not bsnd:
-        raise ValueError(f"TND needs pos_{name}")
-    if gain is not None:
-        tn.gain = _at(gain, f"gain_{name}", index, torch.float32, (D,))
-    if bias is not None:
-        tn.bias = _at(bias, f"bias_{name}", index, torch.float32, (D,))
-    return shape
-
-
-def _qk_call(x_q, x_k, cos_sin, pos_q, pos_k, gain_q, gain_k, bias_q, bias_k, norm_q, norm_k,
-             rot_layout, eps, layout_q, layout_k, status):
-    """(problem, tensors, shape of q, of k, dtype, device index) of either direction; the shape of a
-    side that is None is None."""
-    some = x_q if x_q is not None else x_k
-    if some is None:
-        raise ValueError("x_q and x_k are both None")
-    values, dtype = (some.values if type(some) is Checkpoint else some), some.dtype
-    index, D = values.get_device(), values.shape[-1]
-    if index < 0 or dtype not in _DT or rot_layout not in _ROTS:
-        raise ValueError("CUDA tensors of float16 or bfloat16 and rot_layout halves or pairs are wanted")
-    rot = 0
-    pr, tn = slikl_qk_problem(), slikl_qk_tensors()
-    if cos_sin is not None:
-        pr.table_rows, rot = cos_sin.shape
-        tn.cos_sin = _at(cos_sin, "cos_sin", index, torch.float32)
-    pr.dtype, pr.rot_layout, pr.D, pr.rot_dim, pr.eps = _DT[dtype], _ROTS[rot_layout], D, rot, eps
-    shape_q = shape_k = None
-    if x_q is not None:
-        shape_q = _qk_side(pr.q, tn.q, x_q, "q", layout_q, index, D, dtype, rot, pos_q, gain_q, bias_q, norm_q)
-    else:
-        pr.q.N = 1
-    if x_k is not None:
-        shape_k = _qk_side(pr.k, tn.k, x_k, "k", layout_k, index, D, dtype, rot, pos_k, gain_k, bias_k, norm_k)
-    else:
-        pr.k.N = 1
-    if status is not None:
-        tn.status = _at(status, "status", index, torch.int32, (1,))
-    return pr, tn, shape_q, shape_k, dtype, index
+def _sources(x_q, x_k):
+    """(tensor, scale) of x_q and of x_k, or of their Checkpoints, and the type those stand for."""
+    vq, sq, tq = x_q if type(x_q) is Checkpoint else (x_q, None, None)
+    vk, sk, tk = x_k if type(x_k) is Checkpoint else (x_k, None, None)
+    if tq is not tk and tq is not None and tk is not None:
+        raise ValueError("the checkpoints of q and k must stand for one type")
+    return vq, sq, vk, sk, tq or tk
 
 
 @_on_stream
@@ -858,26 +776,17 @@ def qk_norm_rope(x_q, x_k, cos_sin=None, *, pos_q=None, pos_k=None, gain_q=None,
     in its batch. `status` (int32 [1]) receives SLIKL_DEV_BAD_POSITION. `stream`: as the current one.
     Returns dict(q, k) and, with checkpoint=True, checkpoint_q / checkpoint_k; `out` may supply q, k.
     """
-    pr, tn, shape_q, shape_k, dtype, index = _qk_call(
-        x_q, x_k, cos_sin, pos_q, pos_k, gain_q, gain_k, bias_q, bias_k, norm_q, norm_k, rot_layout,
-        eps, layout_q, layout_k, status)
-    res = dict(q=None, k=None)
-    for name, shape, t in (("q", shape_q, tn.q), ("k", shape_k, tn.k)):
-        if shape is None:
-            continue
-        y = out.get(name) if out else None
-        if y is None:
-            y = torch.empty(shape, dtype=dtype, device=index)
-            t.y = y.data_ptr()
-        else:
-            t.y = _at(y, name, index, dtype, shape)
-        res[name] = y
-        if checkpoint:
-            c = Checkpoint(torch.empty(shape, dtype=torch.float8_e4m3fn, device=index),
-                           torch.empty(shape[:-1], dtype=torch.float32, device=index), dtype)
-            t.keep8, t.keep8_scale = c.values.data_ptr(), c.scale.data_ptr()
-            res["checkpoint_" + name] = c
-    _launch(index, slikl_qk_norm_rope, pr, tn)
+    out_q, out_k = (out.get("q"), out.get("k")) if out else (None, None)
+    rc, q, k, *kept = _load_binding().qk_forward(
+        *_sources(x_q, x_k), cos_sin, pos_q, pos_k, gain_q, gain_k, bias_q, bias_k,
+        _NORMS.get(norm_q, -1), _NORMS.get(norm_k, -1), _ROTS.get(rot_layout, -1), eps,
+        _LAYOUTS.get(layout_q, -1), _LAYOUTS.get(layout_k, -1), True, checkpoint, out_q, out_k, status)
+    if rc != SLIKL_OK:
+        raise SliklError(rc, "slikl_qk_norm_rope")
+    res = dict(q=q, k=k)
+    if checkpoint:
+        res["checkpoint_q"] = Checkpoint(kept[0], kept[1], q.dtype) if q is not None else None
+        res["checkpoint_k"] = Checkpoint(kept[2], kept[3], k.dtype) if k is not None else None
     return res
 
 
@@ -889,93 +798,50 @@ def qk_norm_rope_grad(dq, dk, x_q, x_k, cos_sin=None, *, pos_q=None, pos_k=None,
     the projections. Returns dict(dx_q, dx_k, dgain_q, dgain_k, dbias_q, dbias_k, workspace); a
     side without a norm has no dgain, one without a layer norm no dbias. `out` may supply
     dx_q / dx_k, whose rows may lie apart (slices of one projection's gradient)."""
-    pr, tn, shape_q, shape_k, dtype, index = _qk_call(
-        x_q, x_k, cos_sin, pos_q, pos_k, gain_q, gain_k, None, None, norm_q, norm_k, rot_layout, eps,
-        layout_q, layout_k, status)
-    for name, dy, shape, t in (("dq", dq, shape_q, tn.q), ("dk", dk, shape_k, tn.k)):
-        if shape is not None:
-            if dy is None:
-                raise ValueError(f"{name} is missing")
-            t.dy = _at(dy, name, index, dtype, shape)
-    res = _qk_gradients(pr, tn, shape_q, shape_k, dtype, index, out)
-    nbytes = slikl_qk_norm_rope_grad_workspace_size(pr)
-    if workspace is None or workspace.numel() < nbytes:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=index)
-    _launch(index, slikl_qk_norm_rope_grad, pr, tn, workspace.data_ptr(), workspace.numel())
-    res["workspace"] = workspace
-    return res
-
-
-def _qk_gradients(pr, tn, shape_q, shape_k, dtype, index, out):
-    """Allocates (or takes from `out`) dx, dgain and dbias and enters them in the structs."""
-    res = dict(dx_q=None, dx_k=None, dgain_q=None, dgain_k=None, dbias_q=None, dbias_k=None)
-    # the sums of a side are the rows of one tensor
-    norm_q = pr.q.norm if shape_q is not None else 0
-    norm_k = pr.k.norm if shape_k is not None else 0
-    sums = []
-    if norm_q or norm_k:
-        sums = list(torch.empty((norm_q + norm_k, pr.D), dtype=torch.float32, device=index).unbind(0))
-    for name, shape, side, t, norm in (("q", shape_q, pr.q, tn.q, norm_q), ("k", shape_k, pr.k, tn.k, norm_k)):
-        if shape is None:
-            continue
-        dx = out.get("dx_" + name) if out else None
-        if dx is None:
-            dx = torch.empty(shape, dtype=dtype, device=index)
-        elif dx.get_device() != index or dx.dtype is not dtype or dx.shape != shape:
-            raise ValueError(f"dx_{name} must be {dtype} {tuple(shape)} on cuda:{index}")
-        else:
-            side.dx_stride = _row_stride(dx, f"dx_{name}")
-        t.dx = dx.data_ptr()
-        res["dx_" + name] = dx
-        if norm >= SLIKL_NORM_RMS:
-            g = res["dgain_" + name] = sums.pop()
-            t.dgain = g.data_ptr()
-        if norm == SLIKL_NORM_LAYER:
-            g = res["dbias_" + name] = sums.pop()
-            t.dbias = g.data_ptr()
-    return res
+    out_q, out_k = (out.get("dx_q"), out.get("dx_k")) if out else (None, None)
+    rc, dx_q, dx_k, dgain_q, dbias_q, dgain_k, dbias_k, ws = _load_binding().qk_gradient(
+        dq, dk, *_sources(x_q, x_k), cos_sin, pos_q, pos_k, gain_q, gain_k,
+        _NORMS.get(norm_q, -1), _NORMS.get(norm_k, -1), _ROTS.get(rot_layout, -1), eps,
+        _LAYOUTS.get(layout_q, -1), _LAYOUTS.get(layout_k, -1), out_q, out_k, workspace, status)
+    if rc != SLIKL_OK:
+        raise SliklError(rc, "slikl_qk_norm_rope_grad")
+    return dict(dx_q=dx_q, dx_k=dx_k, dgain_q=dgain_q, dgain_k=dgain_k, dbias_q=dbias_q,
+                dbias_k=dbias_k, workspace=ws)
 
 
 @_on_stream
 def checkpoint_pack(x) -> Checkpoint:
     """8-bit checkpoint of x [.., N, D] (float16 or bfloat16, contiguous, D 64 or 128): one e4m3
     value an element and one fp32 scale, max|x| / 448, for each of the D-long rows."""
-    index = x.get_device()
-    if index < 0:
-        raise ValueError("x must be a CUDA tensor")
-    pr, tn = _rows_problem(x, x.dtype)
-    c = Checkpoint(torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=index),
-                   torch.empty(x.shape[:-1], dtype=torch.float32, device=index), x.dtype)
-    tn.q.x = _at(x, "x", index, x.dtype)
-    tn.q.keep8, tn.q.keep8_scale = c.values.data_ptr(), c.scale.data_ptr()
-    _launch(index, slikl_qk_norm_rope, pr, tn)
-    return c
+    rows = _rows(x)
+    rc, _, _, values, scale, _, _ = _load_binding().qk_forward(
+        rows, None, None, None, None, None, None, None, None, None, None, None, SLIKL_NORM_NONE,
+        SLIKL_NORM_NONE, SLIKL_ROT_HALVES, 1.0, SLIKL_TND, SLIKL_TND, False, True, None, None, None)
+    if rc != SLIKL_OK:
+        raise SliklError(rc, "slikl_qk_norm_rope")
+    return Checkpoint(values.view(x.shape), scale.view(x.shape[:-1]), x.dtype)
 
 
 @_on_stream
 def checkpoint_unpack(c: Checkpoint) -> torch.Tensor:
     """The tensor that a checkpoint stands for, scale * values rounded to its 16-bit type."""
-    index = c.values.get_device()
-    if index < 0:
-        raise ValueError("tensors must be CUDA tensors")
-    pr, tn = _rows_problem(c.values, c.dtype)
-    tn.q.x8 = _at(c.values, "values", index, torch.float8_e4m3fn)
-    tn.q.x8_scale = _at(c.scale, "scale", index, torch.float32, c.values.shape[:-1])
-    x = torch.empty(c.values.shape, dtype=c.dtype, device=index)
-    tn.q.y = x.data_ptr()
-    _launch(index, slikl_qk_norm_rope, pr, tn)
-    return x
+    rows = _rows(c.values)
+    if c.scale.shape != c.values.shape[:-1] or not c.scale.is_contiguous():
+        raise ValueError("scale must be a contiguous tensor of the values' rows")
+    rc, x, *_ = _load_binding().qk_forward(
+        rows, c.scale.view(rows.shape[:-1]), None, None, c.dtype, None, None, None, None, None, None,
+        None, SLIKL_NORM_NONE, SLIKL_NORM_NONE, SLIKL_ROT_HALVES, 1.0, SLIKL_TND, SLIKL_TND, True,
+        False, None, None, None)
+    if rc != SLIKL_OK:
+        raise SliklError(rc, "slikl_qk_norm_rope")
+    return x.view(c.values.shape)
 
 
-def _rows_problem(t, dtype):
-    """A problem of t's D-long rows as they are: neither norm nor rotation."""
-    if dtype not in _DT or t.dim() < 2:
-        raise ValueError("float16 or bfloat16 [.., N, D] is wanted")
-    D = t.shape[-1]
-    return (slikl_qk_problem(_DT[dtype], SLIKL_ROT_HALVES, D, 0, 0, 1.0, 0,
-                             slikl_qk_side(t.numel() // max(D, 1), 1, 1, 0, 0, SLIKL_NORM_NONE, 0),
-                             slikl_qk_side(0, 1, 1, 0, 0, SLIKL_NORM_NONE, 0)),
-            slikl_qk_tensors())
+def _rows(t):
+    """t [.., N, D] as rows of one head."""
+    if t.dim() < 2 or not t.is_contiguous():
+        raise ValueError("a contiguous tensor [.., N, D] is wanted")
+    return t.view(-1, 1, t.shape[-1]) if t.numel() else t.new_empty(0, 1, t.shape[-1])
 
 
 @_on_stream
@@ -991,55 +857,20 @@ def grad_projected(x_q, x_k, w, attn_softmax_l1norm, sparse_indices, cos_sin=Non
     softmax_out, workspace[, loss]); `out` may supply dx_q / dx_k."""
     if x_q is None or x_k is None:
         raise ValueError("x_q and x_k are both needed")
-    qk, qt, sq, sk, dtype, index = _qk_call(
-        x_q, x_k, cos_sin, pos_q, pos_k, gain_q, gain_k, bias_q, bias_k, norm_q, norm_k, rot_layout,
-        eps, layout_q, layout_k, None)
-    i32, f32 = torch.int32, torch.float32
-    pr = slikl_problem(_DT[dtype], _LAYOUTS[layout_q], _LAYOUTS[layout_k], 1 if deterministic else 0)
-    pr.T1, pr.T2, pr.N1, pr.D, pr.topk = qk.q.T, qk.k.T, sq[-2], sq[-1], sparse_indices.shape[-1]
-    pr.B = _batches(layout_q, layout_k, sq[0], sk[0], cu_seqlens_q, cu_seqlens_k)
-    if layout_q == "BSND":
-        pr.S1 = sq[1]
-    pr.S2 = sk[1] if layout_k == "BSND" else int(key_range_bound)
-    slots = tuple(sq[:-2]) + (1, pr.topk)
-    tn = slikl_tensors()
-    tn.w = _at(w, "w", index, f32, sq[:-1])
-    tn.attn_softmax_l1norm = _at(attn_softmax_l1norm, "attn_softmax_l1norm", index, f32, slots)
-    tn.sparse_indices = _at(sparse_indices, "sparse_indices", index, i32, slots)
-    if layout_q == "TND":
-        tn.cu_seqlens_q = _at(cu_seqlens_q, "cu_seqlens_q", index, i32)
-    if layout_k == "TND":
-        tn.cu_seqlens_k = _at(cu_seqlens_k, "cu_seqlens_k", index, i32)
-    opt = make_options(dk_path)
-    if seq_used_q is not None:
-        opt.seq_used_q = _at(seq_used_q, "seq_used_q", index, i32, (pr.B,))
-    if seq_used_k is not None:
-        opt.seq_used_k = _at(seq_used_k, "seq_used_k", index, i32, (pr.B,))
-    res = _qk_gradients(qk, qt, sq, sk, dtype, index, out)
-    res["dw"] = torch.empty(sq[:-1], dtype=f32, device=index)
-    res["softmax_out"] = torch.empty(slots, dtype=f32, device=index)
-    tn.dw, tn.softmax_out = res["dw"].data_ptr(), res["softmax_out"].data_ptr()
+    out_q, out_k = (out.get("dx_q"), out.get("dx_k")) if out else (None, None)
+    rc, dx_q, dx_k, dgain_q, dbias_q, dgain_k, dbias_k, dw, y, losses, ws = _load_binding().grad_projected(
+        *_sources(x_q, x_k), w, attn_softmax_l1norm, sparse_indices, cos_sin, pos_q, pos_k, gain_q,
+        gain_k, bias_q, bias_k, _NORMS.get(norm_q, -1), _NORMS.get(norm_k, -1), _ROTS.get(rot_layout, -1),
+        eps, _LAYOUTS.get(layout_q, -1), _LAYOUTS.get(layout_k, -1), cu_seqlens_q, cu_seqlens_k,
+        deterministic, _DK_PATHS[dk_path], key_range_bound, loss, seq_used_q, seq_used_k, out_q, out_k,
+        workspace)
+    if rc != SLIKL_OK:
+        raise SliklError(rc, "slikl_grad_projected")
+    res = dict(dx_q=dx_q, dx_k=dx_k, dgain_q=dgain_q, dgain_k=dgain_k, dbias_q=dbias_q, dbias_k=dbias_k,
+               dw=dw, softmax_out=y, workspace=ws)
     if loss:
-        res["loss"] = torch.empty(pr.T1, dtype=f32, device=index)
-        opt.loss = res["loss"].data_ptr()
-    nbytes = slikl_grad_projected_workspace_size(pr, qk, opt)
-    if workspace is None or workspace.numel() < nbytes:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=index)
-
-    def call(stream):
-        slikl_grad_projected(pr, qk, tn, qt, workspace.data_ptr(), workspace.numel(), stream, opt)
-    _launch(index, call)
-    res["workspace"] = workspace
+        res["loss"] = losses
     return res
-
-
-def _batches(layout_q, layout_k, rows_q, rows_k, cu_q, cu_k):
-    """The number of batches, on which both sides have to agree."""
-    said = [cu.numel() - 1 if layout == "TND" and cu is not None else rows if layout == "BSND" else -1
-            for layout, rows, cu in ((layout_q, rows_q, cu_q), (layout_k, rows_k, cu_k))]
-    if said[0] != said[1] or said[0] < 0:
-        raise ValueError("queries and keys must have the same number of batches (TND: cu_seqlens)")
-    return said[0]
 
 
 # --- weights on the keys, and a cache cut to them -----------------------------------------------
@@ -1077,49 +908,12 @@ def key_weights(weights, sparse_indices, scores, *, decay=1.0, layout_q="BSND", 
     (slikl_key_weights): fp32 `weights` and int32 `sparse_indices` [B,S1,1,topk] / [T1,1,topk] (p of
     grad(), softmax_out, or p of grad_recompute_p), fp32 `scores` [B,S2] / [T2]. `out` may be
     `scores`. `status` (int32 [1]) receives the device flags. Returns dict(scores, workspace)."""
-    index, i32, f32 = scores.get_device(), torch.int32, torch.float32
-    if index < 0 or layout_q not in _LAYOUTS or layout_k not in _LAYOUTS:
-        raise ValueError("CUDA tensors and layouts BSND or TND are wanted")
-    shape, rows = sparse_indices.shape, scores.shape
-    if len(shape) != (4 if layout_q == "BSND" else 3) or shape[-2] != 1 or \
-            len(rows) != (2 if layout_k == "BSND" else 1):
-        raise ValueError("sparse_indices must be [B,S1,1,topk] / [T1,1,topk], scores [B,S2] / [T2]")
-    pr, tn = slikl_problem(), slikl_key_weights_tensors()
-    pr.topk = shape[-1]
-    pr.B = _batches(layout_q, layout_k, shape[0], rows[0], cu_seqlens_q, cu_seqlens_k)
-    if layout_q == "BSND":
-        pr.S1 = shape[1]
-    else:
-        pr.layout_q, pr.T1 = SLIKL_TND, shape[0]
-        tn.cu_seqlens_q = _at(cu_seqlens_q, "cu_seqlens_q", index, i32)
-    if layout_k == "BSND":
-        pr.S2 = rows[1]
-    else:
-        pr.layout_k, pr.T2, pr.S2 = SLIKL_TND, rows[0], int(key_range_bound)
-        tn.cu_seqlens_k = _at(cu_seqlens_k, "cu_seqlens_k", index, i32)
-    opt = None
-    if seq_used_q is not None or seq_used_k is not None:
-        opt = slikl_options()
-        if seq_used_q is not None:
-            opt.seq_used_q = _at(seq_used_q, "seq_used_q", index, i32, (pr.B,))
-        if seq_used_k is not None:
-            opt.seq_used_k = _at(seq_used_k, "seq_used_k", index, i32, (pr.B,))
-    tn.sparse_indices = _at(sparse_indices, "sparse_indices", index, i32)
-    tn.weights = _at(weights, "weights", index, f32, shape)
-    tn.scores = _at(scores, "scores", index, f32)
-    if status is not None:
-        tn.status = _at(status, "status", index, i32, (1,))
-    if out is None:
-        out = torch.empty_like(scores)
-    tn.out = _at(out, "out", index, f32, rows)
-    nbytes = slikl_key_weights_workspace_size(pr)
-    if workspace is None or workspace.numel() < nbytes:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=index)
-
-    def call(stream):
-        slikl_key_weights(pr, tn, decay, workspace.data_ptr(), workspace.numel(), stream, opt)
-    _launch(index, call)
-    return dict(scores=out, workspace=workspace)
+    rc, new, ws = _load_binding().key_weights(
+        weights, sparse_indices, scores, decay, _LAYOUTS.get(layout_q, -1), _LAYOUTS.get(layout_k, -1),
+        cu_seqlens_q, cu_seqlens_k, seq_used_q, seq_used_k, key_range_bound, out, workspace, status)
+    if rc != SLIKL_OK:
+        raise SliklError(rc, "slikl_key_weights")
+    return dict(scores=new, workspace=ws)
 
 
 @_on_stream
@@ -1132,49 +926,10 @@ def evict(scores, caches: Sequence[torch.Tensor], budget, *, sinks=0, recent=0, 
     rows kept [B] (the seq_used_k of the result), their scores, and the caches [B,budget,..].
     `out` may supply any of the four; rows of its caches behind the last kept one are left as they
     were (without it they are zero)."""
-    index, i32, f32 = scores.get_device(), torch.int32, torch.float32
-    if index < 0 or layout_k not in _LAYOUTS:
-        raise ValueError("CUDA tensors and layout BSND or TND are wanted")
-    rows, bsnd = scores.shape, layout_k == "BSND"
-    lead = len(rows)
-    if lead != (2 if bsnd else 1) or (not bsnd and cu_seqlens_k is None):
-        raise ValueError("scores must be [B,S2], or [T2] with cu_seqlens_k")
-    if budget < 1 or len(caches) > SLIKL_EVICT_MAX_CACHES:
-        raise ValueError(f"budget must be at least 1, and caches at most {SLIKL_EVICT_MAX_CACHES}")
-    pr, tn = slikl_evict_problem(), slikl_evict_tensors()
-    pr.n_caches, pr.budget, pr.sinks, pr.recent = len(caches), budget, sinks, recent
-    if bsnd:
-        pr.B, pr.S2 = rows
-    else:
-        pr.layout_k, pr.B, pr.S2, pr.T2 = SLIKL_TND, cu_seqlens_k.numel() - 1, int(key_range_bound), rows[0]
-        tn.cu_seqlens_k = _at(cu_seqlens_k, "cu_seqlens_k", index, i32)
-    B = pr.B
-    places = (B, budget)
-    tn.scores = _at(scores, "scores", index, f32)
-    if seq_used_k is not None:
-        tn.seq_used_k = _at(seq_used_k, "seq_used_k", index, i32, (B,))
-    if status is not None:
-        tn.status = _at(status, "status", index, i32, (1,))
-    kept = lengths = new = outs = None
-    if out:
-        kept, lengths, new, outs = out.get("kept"), out.get("lengths"), out.get("scores"), out.get("caches")
-    kept = torch.empty(places, dtype=i32, device=index) if kept is None else kept
-    lengths = torch.empty(B, dtype=i32, device=index) if lengths is None else lengths
-    new = torch.empty(places, dtype=f32, device=index) if new is None else new
-    if outs is None:
-        outs = [torch.zeros(places + c.shape[lead:], dtype=c.dtype, device=index) for c in caches]
-    if len(outs) != len(caches):
-        raise ValueError("out['caches'] must have a tensor for each cache")
-    tn.kept = _at(kept, "kept", index, i32, places)
-    tn.lengths = _at(lengths, "lengths", index, i32, (B,))
-    tn.scores_out = _at(new, "scores (out)", index, f32, places)
-    for i, (c, o) in enumerate(zip(caches, outs)):
-        shape = c.shape
-        if shape[:lead] != rows:
-            raise ValueError(f"cache {i} must have scores' rows")
-        rest = shape[lead:]
-        tn.caches[i] = (_at(c, f"cache {i}", index, c.dtype),
-                        _at(o, f"out cache {i}", index, c.dtype, places + rest),
-                        rest.numel() * c.element_size())
-    _launch(index, slikl_evict, pr, tn)
+    get = (out or {}).get
+    rc, kept, lengths, new, outs = _load_binding().evict(
+        scores, caches, budget, sinks, recent, _LAYOUTS.get(layout_k, -1), cu_seqlens_k, seq_used_k,
+        key_range_bound, get("kept"), get("lengths"), get("scores"), get("caches"), status)
+    if rc != SLIKL_OK:
+        raise SliklError(rc, "slikl_evict")
     return dict(kept=kept, lengths=lengths, scores=new, caches=outs)

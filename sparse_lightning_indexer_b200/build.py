@@ -1,4 +1,5 @@
-"""Builds the CUDA library libslikl.so in-tree with nvcc for sm_100a.
+"""Builds the CUDA library libslikl.so in-tree with nvcc for sm_100a, and beside it _slikl_torch.so, the
+C++ marshalling of torch tensors for the calls whose latency counts (g++, no device code).
 
 Usage: python -m sparse_lightning_indexer_b200.build [--force]
 """
@@ -15,6 +16,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libslikl.so")
+TORCH_LIB = os.path.join(PKG, "_slikl_torch.so")
 OBJDIR = os.path.join(PKG, "_build")
 
 NVCC_FLAGS = [
@@ -66,7 +68,35 @@ def build(force: bool = False, verbose: bool = False) -> str:
                *objs, "-lcuda"]
         subprocess.check_call(cmd)
         os.replace(tmp, LIB)
+    build_torch(force)
     return LIB
+
+
+def build_torch(force: bool = False) -> str:
+    """Compile csrc/slikl_torch.cpp against torch's headers and libslikl.so; returns its path."""
+    src = os.path.join(CSRC, "slikl_torch.cpp")
+    headers = glob.glob(os.path.join(INCLUDE, "*.h"))
+    if not force and not _stale(TORCH_LIB, [src] + headers):
+        return TORCH_LIB
+    import sysconfig
+
+    import torch
+    troot = os.path.dirname(torch.__file__)
+    includes = [os.path.join(troot, "include"), os.path.join(troot, "include", "torch", "csrc", "api", "include"),
+                sysconfig.get_paths()["include"],
+                os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")]
+    tmp = TORCH_LIB + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[a for i in includes for a in ("-isystem", i)], "-I", INCLUDE, src, "-o", tmp,
+           "-L", PKG, "-lslikl", "-L", os.path.join(troot, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
+           "-ltorch", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        sys.stderr.write(res.stdout + res.stderr)
+        raise RuntimeError(f"g++ failed on {src}")
+    os.replace(tmp, TORCH_LIB)
+    return TORCH_LIB
 
 
 if __name__ == "__main__":

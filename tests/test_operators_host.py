@@ -310,10 +310,10 @@ def test_binding_refuses_before_any_launch():
                 torch.zeros(4, 1, 64).expand(4, 2, 64), torch.zeros(1, 2, 64).expand(4, 2, 64),
                 torch.zeros(2, 5, 2, 64)[:, :4], torch.zeros(4, 132).view(4, 132)[:, :128].unflatten(1, (2, 64))):
         with pytest.raises(ValueError):
-            sli._row_stride(bad, "x")
+            sli._load_binding().row_stride(bad, "x")
     ok = torch.zeros(4, 200)[:, 8:136].unflatten(1, (2, 64))
-    assert sli._row_stride(ok, "x") == 200 and sli._row_stride(x, "x") == 128
-    assert sli._row_stride(torch.zeros(1, 1, 2, 64).expand(1, 1, 2, 64), "x") == 128
+    assert sli._load_binding().row_stride(ok, "x") == 200 and sli._load_binding().row_stride(x, "x") == 128
+    assert sli._load_binding().row_stride(torch.zeros(1, 1, 2, 64).expand(1, 1, 2, 64), "x") == 128
 
 
 @pytest.mark.skipif(shutil.which("gcc") is None, reason="needs gcc")
