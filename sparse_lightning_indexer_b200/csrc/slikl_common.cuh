@@ -176,6 +176,31 @@ __device__ __forceinline__ int32_t slot_row(int32_t v, int32_t kbase, int32_t kl
 slikl_status check_index_call(const slikl_problem *problem, const slikl_tensors *tensors,
                               const slikl_options *options, bool need_all);
 
+// Launches a kernel that reads what the kernel before it in the stream wrote, so that its blocks may
+// be set up while that one still runs: the earlier kernel calls let_next_start(), and this one
+// await_previous() before it touches memory (it returns when the earlier kernel has ended and its
+// writes are visible).
+template <typename... P, typename... A>
+inline cudaError_t launch_next(void (*kernel)(P...), dim3 grid, unsigned threads, cudaStream_t s,
+                               const A &...args) {
+    cudaLaunchConfig_t c{};
+    c.gridDim = grid;
+    c.blockDim = dim3(threads);
+    c.stream = s;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    c.attrs = &at;
+    c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, kernel, args...);
+}
+__device__ __forceinline__ void let_next_start() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void await_previous() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // kernels (defined in the .cu files)
 cudaError_t launch_metadata(const Params &P, int workers, int mode, cudaStream_t s);
 cudaError_t launch_fused_sm100(const Params &P, int workers, cudaStream_t s);

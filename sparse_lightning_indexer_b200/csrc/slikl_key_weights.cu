@@ -1,8 +1,22 @@
 // The weight that a call's query rows put on each key row (slikl_key_weights; formula and
 // contract in include/slikl.h).
 //
-// Weights are summed as 64-bit integers, so the order of the additions does not change the result.
-// The floor is the read of the slots (an index and a weight, 8 bytes each).
+// Weights are summed as 64-bit integers, so the order of the additions does not change the result. The
+// floor is the read of the slots (an index and a weight, 8 bytes each); what has to be kept from
+// bounding the call instead is the scattered additions. 64-bit additions to global memory, one a
+// slot, run at 128 G/s on B200 however far apart the keys are (147 us for 16.8 M slots over 131072
+// keys, seven times the floor) and slower on few keys. So sums are kept in shared memory, as 32-bit
+// additions that return what was there: a carry out of the low word, and the high word of a large
+// weight, are rare and go their own way. All rows of a batch name the same keys, so a block reads a
+// stretch of the batch's slots without looking where rows begin. Two forms:
+//   weights_direct  few slots a batch (a decoding step): a block owns a chunk of a batch's keys, reads
+//                   all of the batch's slots, keeps both words and writes the chunk's result: one
+//                   launch and no workspace;
+//   weights_split   else: blocks share a batch's slots, keep the low words of up to 55296 keys (larger
+//                   ranges are covered by several blocks that read the same slots, from L2 mostly)
+//                   and add them to 64-bit sums in the workspace once; weights_finish makes the result.
+#include <algorithm>
+
 #include "slikl_common.cuh"
 
 namespace slikl {
@@ -17,6 +31,7 @@ struct WeightArgs {
     float decay;
     float one;                // 2^u: the units of a weight of 1
     unsigned long long *sums; // [T2], in units
+    int64_t first_batch;      // of weights_split's grid
     uint32_t *status;
 };
 
@@ -24,33 +39,15 @@ __device__ __forceinline__ void flag(const WeightArgs &a, uint32_t bit) {
     if (a.status) set_status(a.status, bit);
 }
 
-// The keys that query row t's slots may name: rows [base, base + used) of the key tensor, of the
-// `count` that its batch has.
-struct RowKeys {
-    int64_t base;
+// A batch's slots [begin, end) of its rows in use, and the keys that they may name: rows [base, base +
+// used) of the key tensor, of the `count` that the batch has. Empty where cu_seqlens is unusable.
+struct Batch {
+    int64_t begin, end, base;
     int32_t count, used;
-    bool in_use;              // a row whose indices are read
 };
 
-__device__ RowKeys row_keys(const WeightArgs &a, int64_t t) {
-    RowKeys r{0, 0, 0, false};
-    int64_t b, q0, q1;
-    if (a.layout_q == SLIKL_BSND) {
-        b = t / a.S1;
-        q0 = b * a.S1;
-        q1 = q0 + a.S1;
-    } else {
-        int64_t lo = 0, hi = a.B - 1;       // the last batch that begins at or before t
-        while (lo < hi) {
-            const int64_t mid = (lo + hi + 1) >> 1;
-            if (a.cu_q[mid] <= t) lo = mid; else hi = mid - 1;
-        }
-        b = lo;
-        q0 = a.cu_q[b];
-        q1 = a.cu_q[b + 1];
-        if (t < q0 || t >= q1) return r;
-    }
-    if (a.used_q && t - q0 >= a.used_q[b]) return r;
+__device__ Batch batch_of(const WeightArgs &a, int64_t b) {
+    Batch r{0, 0, 0, 0, 0};
     if (a.layout_k == SLIKL_BSND) {
         r.base = b * a.S2;
         r.count = (int32_t)a.S2;
@@ -60,39 +57,128 @@ __device__ RowKeys row_keys(const WeightArgs &a, int64_t t) {
         r.base = k0;
         r.count = (int32_t)(k1 - k0);
     }
-    r.in_use = true;
-    r.used = r.count;
-    if (a.used_k) r.used = max(0, min(a.used_k[b], r.count));
+    r.used = a.used_k ? max(0, min(a.used_k[b], r.count)) : r.count;
+    int64_t q0, qn;
+    if (a.layout_q == SLIKL_BSND) {
+        q0 = b * a.S1;
+        qn = a.S1;
+    } else {
+        q0 = a.cu_q[b];
+        qn = a.cu_q[b + 1] - q0;
+        if (q0 < 0 || qn < 0 || q0 + qn > a.T1) return r;
+    }
+    if (a.used_q) qn = max((int64_t)0, min((int64_t)a.used_q[b], qn));
+    r.begin = q0 * a.K;
+    r.end = (q0 + qn) * a.K;
     return r;
 }
 
 // A weight in units of 2^-u.
-__device__ __forceinline__ unsigned long long units(const WeightArgs &a, float w) {
+__device__ __forceinline__ uint64_t units(const WeightArgs &a, float w) {
     if (!(w >= 0.f && w <= 2.f)) {
         flag(a, SLIKL_DEV_BAD_WEIGHT);
         w = w > 2.f ? 2.f : 0.f;
     }
-    return (unsigned long long)__float2ll_rn(w * a.one);
+    return (uint64_t)__float2ll_rn(w * a.one);
 }
 
-// Whether a slot of a row in use names one of its keys; flags an index that breaks the contract.
-__device__ __forceinline__ bool names_key(const WeightArgs &a, const RowKeys &r, int32_t v) {
-    if (v < -1 || v >= r.count) flag(a, SLIKL_DEV_INDEX_OUT_OF_RANGE);
-    return v >= 0 && v < r.used;
+// Adds n to the shared word at `at` and returns what was there; 0 where `take` is false.
+__device__ __forceinline__ uint32_t add_low(uint32_t at, uint32_t n, bool take = true) {
+    uint32_t was = 0;
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %3, 0;\n\t"
+                 "@p atom.shared.add.u32 %0, [%1], %2;\n\t}"
+                 : "+r"(was)
+                 : "r"(at), "r"(n), "r"((uint32_t)take)
+                 : "memory");
+    return was;
 }
 
-__global__ void __launch_bounds__(256) weights_scatter(WeightArgs a) {
-    const int lane = threadIdx.x & 31;
-    for (int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); t < a.T1;
-         t += (int64_t)gridDim.x * 8) {
-        const RowKeys r = row_keys(a, t);
-        if (!r.in_use) continue;
-        const int64_t o = t * a.K;
-        for (int j = lane; j < a.K; j += 32) {
-            const int32_t v = a.idx[o + j];
-            if (names_key(a, r, v)) atomicAdd(a.sums + r.base + v, units(a, a.weights[o + j]));
+// Adds the weights of the slots of [begin, end) that name a key of [first, first + keys) to the low
+// words; more(key, n) adds n times 2^32. Flags indices that break the contract.
+//
+// A thread takes kAtOnce slots at a time, a block's width apart: neighbouring threads hold neighbouring
+// slots, whose keys, where a row is sorted, meet in few banks. Loads run ahead: the indices two such
+// steps, the weights (read only where the slot counts) one, since their latency was what the plain
+// loop spent its time on. Carries, weights of 2^(32-u) and more and bad ones are seen to behind the
+// step's additions, together.
+constexpr int kAtOnce = 4;
+
+template <int THREADS, typename F>
+__device__ __forceinline__ void add_slots(const WeightArgs &a, const Batch &r, int64_t begin,
+                                          int64_t end, int32_t first, int32_t keys, uint32_t *low,
+                                          F more) {
+    constexpr int N = kAtOnce;
+    constexpr uint32_t STEP = N * THREADS;
+    const uint32_t named = (uint32_t)max(0, min(keys, r.used - first)), count = r.count;
+    const uint32_t slots = (uint32_t)(end - begin), at = (uint32_t)__cvta_generic_to_shared(low);
+    const int32_t *idx = a.idx + begin;
+    const float *weights = a.weights + begin;
+    const uint32_t small = __float_as_uint(4294967296.f);     // bits of 0 <= x < 2^32 are below
+    uint32_t largest = 0;     // of the indices plus one
+    // (indices as keys of the chunk: those outside it are at least `named`)
+    auto indices = [&](uint32_t i, uint32_t *v) {
+        const int32_t *p = idx + i;
+        if (i + (N - 1) * THREADS < slots) {
+#pragma unroll
+            for (int k = 0; k < N; ++k) v[k] = p[k * THREADS];
+        } else {
+#pragma unroll
+            for (int k = 0; k < N; ++k) v[k] = i + k * THREADS < slots ? p[k * THREADS] : -1;
+        }
+    };
+    auto scaled = [&](uint32_t i, uint32_t *v, float *w) {
+        const float *p = weights + i;
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            largest = max(largest, v[k] + 1);
+            v[k] -= first;
+            w[k] = v[k] < named ? p[k * THREADS] : 0.f;
+        }
+    };
+    auto add = [&](const uint32_t *v, const float *w) {
+        // (rows are sorted more often than not, and all of a warp's slots outside the chunk then)
+        bool some = false;
+#pragma unroll
+        for (int k = 0; k < N; ++k) some |= v[k] < named;
+        if (!__any_sync(0xffffffffu, some)) return;
+        uint32_t rare = 0;
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const float x = w[k] * a.one;
+            const bool odd = __float_as_uint(x) >= small;
+            const uint32_t lo = __float2uint_rn(x);
+            const uint32_t was = add_low(at + 4 * v[k], lo, v[k] < named && !odd);
+            if (odd || was > ~lo) rare |= 1u << k;           // ... or a carry
+        }
+        if (!rare) return;
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            if (!(rare >> k & 1) || v[k] >= named) continue;
+            uint32_t hi = 1;
+            if (__float_as_uint(w[k] * a.one) >= small) {
+                const uint64_t u = units(a, w[k]);
+                const uint32_t lo = (uint32_t)u;
+                hi = (uint32_t)(u >> 32) + (add_low(at + 4 * v[k], lo) > ~lo);
+            }
+            if (hi) more(v[k], hi);
+        }
+    };
+    uint32_t v[3][N];
+    float w[2][N];
+    uint32_t i = threadIdx.x;
+    indices(i, v[0]);
+    indices(i + STEP, v[1]);
+    scaled(i, v[0], w[0]);
+    for (uint32_t all = 0; all < slots; all += 6 * STEP, i += 6 * STEP) {   // the same steps for all threads
+#pragma unroll
+        for (int j = 0; j < 6; ++j) {
+            if (j && all + j * STEP >= slots) break;
+            indices(i + (j + 2) * STEP, v[(j + 2) % 3]);
+            scaled(i + (j + 1) * STEP, v[(j + 1) % 3], w[(j + 1) % 2]);
+            add(v[j % 3], w[j % 2]);
         }
     }
+    if (largest > count) flag(a, SLIKL_DEV_INDEX_OUT_OF_RANGE);
 }
 
 // What the per-batch arrays promise, looked at once by the first block of weights_finish.
@@ -124,7 +210,58 @@ __device__ __forceinline__ float finished(const WeightArgs &a, unsigned long lon
     return (float)s;
 }
 
+constexpr int kDirectThreads = 512, kDirectKeys = 2048;
+constexpr int kSplitThreads = 1024, kSplitKeys = 55296;       // 216 KB of low words
+
+// grid (chunks of keys, batches).
+__global__ void __launch_bounds__(kDirectThreads) weights_direct(WeightArgs a, int chunk) {
+    __shared__ uint32_t low[kDirectKeys], high[kDirectKeys];
+    const int64_t b = blockIdx.y;
+    if (blockIdx.x == 0 && b == 0 && a.status) check_batches(a);
+    const Batch r = batch_of(a, b);
+    for (int64_t first = (int64_t)blockIdx.x * chunk; first < r.count;
+         first += (int64_t)gridDim.x * chunk) {
+        const int32_t keys = (int32_t)min((int64_t)chunk, r.count - first);
+        for (int i = threadIdx.x; i < keys; i += kDirectThreads) low[i] = high[i] = 0;
+        __syncthreads();
+        add_slots<kDirectThreads>(a, r, r.begin, r.end, (int32_t)first, keys, low,
+                  [&](int32_t k, uint32_t n) { atomicAdd(&high[k], n); });
+        __syncthreads();
+        for (int i = threadIdx.x; i < keys; i += kDirectThreads) {
+            const int64_t key = r.base + first + i;
+            a.out[key] = finished(a, (unsigned long long)high[i] << 32 | low[i], key);
+        }
+        __syncthreads();
+    }
+}
+
+// grid (chunks of keys, splits of the slots, batches). Blocks next to one another read the same slots.
+__global__ void __launch_bounds__(kSplitThreads) weights_split(WeightArgs a, int chunk) {
+    extern __shared__ uint32_t low[];
+    let_next_start();         // weights_finish
+    const Batch r = batch_of(a, a.first_batch + blockIdx.z);
+    const int64_t slots = r.end - r.begin;
+    const int64_t begin = r.begin + slots * blockIdx.y / gridDim.y;
+    const int64_t end = r.begin + slots * (blockIdx.y + 1) / gridDim.y;
+    if (begin == end) return;
+    for (int64_t first = (int64_t)blockIdx.x * chunk; first < r.used;
+         first += (int64_t)gridDim.x * chunk) {
+        const int32_t keys = (int32_t)min((int64_t)chunk, r.used - first);
+        unsigned long long *sums = a.sums + r.base + first;
+        for (int i = threadIdx.x; i < keys; i += kSplitThreads) low[i] = 0;
+        __syncthreads();
+        add_slots<kSplitThreads>(a, r, begin, end, (int32_t)first, keys, low, [&](int32_t k, uint32_t n) {
+            atomicAdd(sums + k, (unsigned long long)n << 32);
+        });
+        __syncthreads();
+        for (int i = threadIdx.x; i < keys; i += kSplitThreads)
+            if (low[i]) atomicAdd(sums + i, (unsigned long long)low[i]);
+        __syncthreads();
+    }
+}
+
 __global__ void __launch_bounds__(256) weights_finish(WeightArgs a) {
+    await_previous();
     if (blockIdx.x == 0 && a.status) check_batches(a);
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i < a.T2) a.out[i] = finished(a, a.sums[i], i);
@@ -198,10 +335,10 @@ slikl_status slikl_key_weights(const slikl_problem *problem,
         return SLIKL_ERR_PARAM_INVALID;
     const Layout L = make_workspace(T2);
     if (workspace_bytes < L.total) return SLIKL_ERR_WORKSPACE_TOO_SMALL;
-    int dev = 0, major = 0;
+    int dev = 0, major = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-        major != 10)
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || major != 10)
         return SLIKL_ERR_CUDA;
     if (T2 == 0) return SLIKL_OK;
 
@@ -231,15 +368,44 @@ slikl_status slikl_key_weights(const slikl_problem *problem,
     a.status = tensors->status;
 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    // longest key range: known, promised, or all keys
+    const int64_t range = std::min(pr.S2 > 0 ? pr.S2 : T2, T2);
+    // A block of the direct form reads every slot of its batch, so that form is for few of them: up to
+    // 65536 a batch (on average, where lengths differ) its time stays below the other form's three
+    // launches.
+    if (T1 * pr.topk <= 65536 * pr.B && pr.B <= 65535) {
+        // chunks of 256 to 2048 keys, two blocks a multiprocessor where there are as many
+        int64_t chunk = 256;
+        while (chunk < kDirectKeys && pr.B * ((range + chunk - 1) / chunk) > 2 * sms) chunk *= 2;
+        const int64_t chunks = std::min<int64_t>((range + chunk - 1) / chunk, 1 << 20);
+        weights_direct<<<dim3((unsigned)chunks, (unsigned)pr.B), kDirectThreads, 0, s>>>(a, (int)chunk);
+        return cudaGetLastError() == cudaSuccess ? SLIKL_OK : SLIKL_ERR_CUDA;
+    }
     if (cudaMemsetAsync(a.sums, 0, sizeof(*a.sums) * (size_t)T2, s) != cudaSuccess)
         return SLIKL_ERR_CUDA;
     if (T1 > 0) {
-        const int64_t blocks = (T1 + 7) / 8;
-        weights_scatter<<<(unsigned)(blocks < 148 * 8 ? blocks : 148 * 8), 256, 0, s>>>(a);
-        if (cudaGetLastError() != cudaSuccess) return SLIKL_ERR_CUDA;
+        const int64_t chunks = (range + kSplitKeys - 1) / kSplitKeys;
+        const int64_t chunk = (range + chunks - 1) / chunks;
+        const size_t smem = sizeof(uint32_t) * (size_t)chunk;
+        // as many splits as fill the multiprocessors, each of 4096 slots at least
+        const int64_t per_sm = smem > 100 * 1024 ? 1 : 2;
+        const int64_t splits = std::max<int64_t>(
+            1, std::min(sms * per_sm / (chunks * pr.B), (T1 * pr.topk / pr.B + 4095) / 4096));
+        if (cudaFuncSetAttribute(weights_split, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)(sizeof(uint32_t) * kSplitKeys)) != cudaSuccess)
+            return SLIKL_ERR_CUDA;
+        WeightArgs part = a;
+        // the grid's third dimension holds 65535 batches
+        for (int64_t b = 0; b < pr.B; b += 65535) {
+            part.first_batch = b;
+            weights_split<<<dim3((unsigned)chunks, (unsigned)splits, (unsigned)std::min<int64_t>(pr.B - b, 65535)),
+                            kSplitThreads, smem, s>>>(part, (int)chunk);
+            if (cudaGetLastError() != cudaSuccess) return SLIKL_ERR_CUDA;
+        }
     }
-    weights_finish<<<(unsigned)((T2 + 255) / 256), 256, 0, s>>>(a);
-    return cudaGetLastError() == cudaSuccess ? SLIKL_OK : SLIKL_ERR_CUDA;
+    return launch_next(weights_finish, dim3((unsigned)((T2 + 255) / 256)), 256, s, a) == cudaSuccess
+               ? SLIKL_OK
+               : SLIKL_ERR_CUDA;
 }
 
 }  // extern "C"

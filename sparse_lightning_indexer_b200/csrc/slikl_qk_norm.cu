@@ -807,6 +807,7 @@ template <typename T, int D, bool PAIRS>
 __global__ void __launch_bounds__(kThreads, kGradPerSm) qk_gradient(const __grid_constant__ Args a) {
     __shared__ __align__(16) unsigned char smem[kRingBytes<true>];
     __shared__ float4 gains[D / 4];
+    let_next_start();         // qk_grad_sums
     const bool k = blockIdx.x >= a.blocks_q;
     const Side &s = a.side[k];
     const uint32_t block = blockIdx.x - (k ? a.blocks_q : 0);
@@ -830,6 +831,7 @@ struct Sums {
 // One block adds 32 columns of one of the four sums over the blocks' partial sums.
 __global__ void __launch_bounds__(1024) qk_grad_sums(Sums a) {
     __shared__ float smem[32][33];
+    await_previous();
     const int which = blockIdx.y, col = blockIdx.x * 32 + (threadIdx.x & 31), part = threadIdx.x >> 5;
     if (!a.out[which]) return;
     // eight loads on the way at once: one after another they took 4 us
@@ -1043,8 +1045,8 @@ slikl_status run_gradient(const slikl_qk_problem *p, const slikl_qk_tensors *t, 
               {a.blocks_q, a.blocks_q, a.blocks_k, a.blocks_k},
               partial, (int)p->D};
     if (sums.out[0] || sums.out[1] || sums.out[2] || sums.out[3]) {
-        qk_grad_sums<<<dim3((unsigned)p->D / 32, 4), 1024, 0, st>>>(sums);
-        if (cudaGetLastError() != cudaSuccess) return SLIKL_ERR_CUDA;
+        if (launch_next(qk_grad_sums, dim3((unsigned)p->D / 32, 4), 1024, st, sums) != cudaSuccess)
+            return SLIKL_ERR_CUDA;
     }
     return SLIKL_OK;
 }
