@@ -3,7 +3,14 @@
 //
 // evict_choose finds, for each sequence, the score of the last row that stays by a radix select
 // over order-preserving integers (three passes of 11, 11 and 10 bits), then walks the rows in
-// order and writes the kept ones behind one another. evict_copy moves the caches' rows.
+// order and writes the kept ones behind one another. It is bound by latency: a pass over the scores,
+// which L2 holds, and the barriers between. So a long sequence is shared by a cluster of eight blocks,
+// whose histograms and counts the others read from its shared memory (one block took 127 us for
+// sequences of up to 131072 rows). evict_copy moves the caches' rows, bound by HBM.
+#include <cooperative_groups.h>
+
+#include <algorithm>
+
 #include "slikl_common.cuh"
 
 namespace slikl {
@@ -57,8 +64,8 @@ __device__ __forceinline__ uint32_t order_of(float x) {
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// Exclusive prefix of v over the block and the block's total.
-__device__ int block_prefix(int v, int *warp_sums, int &total) {
+// Exclusive prefix of v over the block.
+__device__ int block_prefix(int v, int *warp_sums) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int x = v;
 #pragma unroll
@@ -66,104 +73,221 @@ __device__ int block_prefix(int v, int *warp_sums, int &total) {
         const int y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
     }
-    __syncthreads();
     if (lane == 31) warp_sums[warp] = x;
     __syncthreads();
     if (warp == 0) {
-        int w = warp_sums[lane];
+        const int own = warp_sums[lane];
+        int w = own;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int y = __shfl_up_sync(0xffffffffu, w, o);
             if (lane >= o) w += y;
         }
-        warp_sums[lane] = w;
+        warp_sums[lane] = w - own;
     }
     __syncthreads();
-    total = warp_sums[31];
-    return x - v + (warp ? warp_sums[warp - 1] : 0);
+    return x - v + warp_sums[warp];
 }
 
-__global__ void __launch_bounds__(kChoose) evict_choose(EvictArgs a) {
-    __shared__ int bins[kBins];
-    __shared__ int warp_sums[32];
+// Rows [j0, j0 + 32 * rounds) of a warp's share, a round 32 neighbours; at most kRounds rounds a tile.
+constexpr int kRounds = 16;
+
+template <int CS>
+__global__ void __launch_bounds__(kChoose) __cluster_dims__(CS, 1, 1) evict_choose(EvictArgs a) {
+    namespace cg = cooperative_groups;
+    __shared__ int bins[3][kBins];       // of each pass: the other blocks may still read an earlier one
+    __shared__ int warp_sums[32], more[2][32];
     __shared__ uint32_t found_bin;
-    __shared__ int found_above;
-    const int64_t b = blockIdx.x;
-    const Sequence q = sequence_of(a, b, threadIdx.x == 0);
-    const int32_t n = q.n, stay = min(n, a.budget);
-    const bool all = n <= a.budget;
-    const int32_t lo = all ? 0 : a.sinks, hi = all ? 0 : n - a.recent;   // rows that scores decide on
-    const int32_t wanted = all ? 0 : a.budget - a.sinks - a.recent;
+    __shared__ int found_above, counts[2];
+    let_next_start();                    // evict_copy
+    auto cluster = cg::this_cluster();
+    const uint32_t rank = CS == 1 ? 0 : cluster.block_rank();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t b = blockIdx.x / CS;
+    const Sequence q = sequence_of(a, b, threadIdx.x == 0 && rank == 0);
+    const uint32_t n = q.n, budget = a.budget, stay = min(n, budget);
+    const bool all = n <= budget;
+    const uint32_t lo = all ? 0 : a.sinks, hi = all ? 0 : n - a.recent;   // rows that scores decide on
+    const uint32_t wanted = all ? 0 : budget - a.sinks - a.recent;
     const float *scores = a.scores + q.base;
+    // the block's slice of the rows, and its warps' shares of a tile of it
+    const uint32_t per = (n + CS - 1) / CS, slice0 = min(n, rank * per), slice1 = min(n, slice0 + per);
+    const int rounds = min((slice1 - slice0 + kChoose - 1) / kChoose, (uint32_t)kRounds);
+    const uint32_t share = 32 * rounds, tile = 32 * share;
 
     // the order number of the wanted-th of them, and how many rows with that number stay
     uint32_t prefix = 0, mask = 0;
-    int left = wanted;
+    int left = wanted, above_mine = 0;
     if (wanted > 0) {
+        for (int i = threadIdx.x; i < 3 * kBins; i += kChoose) bins[0][i] = 0;
+        __syncthreads();
         for (int pass = 0; pass < 3; ++pass) {
             const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, width = pass == 2 ? 10 : 11;
-            for (int i = threadIdx.x; i < kBins; i += kChoose) bins[i] = 0;
-            __syncthreads();
-            for (int32_t j = lo + threadIdx.x; j < hi; j += kChoose) {
-                const uint32_t o = order_of(scores[j]);
-                if ((o & mask) == prefix) atomicAdd(&bins[(o >> shift) & ((1u << width) - 1)], 1);
+            // (eight loads on the way at once)
+            const uint32_t end = min(hi, slice1);
+            for (uint32_t j = max(lo, slice0) + threadIdx.x; j < end; j += 8 * kChoose) {
+                float x[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = j + i * kChoose < end ? scores[j + i * kChoose] : 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t o = order_of(x[i]);
+                    if (j + i * kChoose < end && (o & mask) == prefix)
+                        atomicAdd(&bins[pass][(o >> shift) & ((1u << width) - 1)], 1);
+                }
             }
-            __syncthreads();
+            if (CS == 1) __syncthreads();
+            else cluster.sync();
             // thread i holds bins 2047 - 2i and 2046 - 2i: the prefix runs from the highest bin
-            const int h0 = bins[kBins - 1 - 2 * threadIdx.x], h1 = bins[kBins - 2 - 2 * threadIdx.x];
-            int total;
-            const int above = block_prefix(h0 + h1, warp_sums, total);
+            const int bin = kBins - 2 - 2 * threadIdx.x;
+            int h1 = 0, h0 = 0, m1 = bins[pass][bin], m0 = bins[pass][bin + 1];
+            if (CS == 1) {
+                h1 = m1, h0 = m0;
+            } else {
+#pragma unroll
+                for (int r = 0; r < CS; ++r) {
+                    const int2 h = *reinterpret_cast<const int2 *>(cluster.map_shared_rank(&bins[pass][bin], r));
+                    h1 += h.x, h0 += h.y;
+                }
+            }
+            const int above = block_prefix(h0 + h1, warp_sums);
             if (above < left && left <= above + h0 + h1) {
                 const bool first = left <= above + h0;
-                found_bin = kBins - 1 - 2 * threadIdx.x - (first ? 0 : 1);
+                found_bin = bin + (first ? 1 : 0);
                 found_above = above + (first ? 0 : h0);
             }
             __syncthreads();
-            prefix |= found_bin << shift;
+            const int found = found_bin;
+            above_mine += (bin > found ? m1 : 0) + (bin + 1 > found ? m0 : 0);
+            prefix |= (uint32_t)found << shift;
             mask |= ((1u << width) - 1) << shift;
             left -= found_above;
-            __syncthreads();
+        }
+    }
+    // rows before this block's slice that stay whatever the ties (counts[0]) or tie for the last
+    // places (counts[1])
+    int sure = 0, tied = 0;
+    if (CS > 1) {
+        const int total = block_prefix(above_mine, warp_sums) + above_mine;
+        if (threadIdx.x == kChoose - 1) {
+            const uint32_t from = max(lo, slice0), to = min(hi, slice1);
+            const uint32_t inside = from < to ? to - from : 0;
+            counts[0] = total + (int)(slice1 - slice0 - inside);
+            counts[1] = wanted > 0 ? bins[2][prefix & 1023] : 0;
+        }
+        cluster.sync();
+        for (int r = 0; r < (int)rank; ++r) {
+            const int *c = cluster.map_shared_rank(counts, r);
+            sure += c[0];
+            tied += c[1];
         }
     }
 
-    int32_t *kept = a.kept + b * a.budget;
-    float *out = a.scores_out ? a.scores_out + b * a.budget : nullptr;
-    int at = 0, equals = 0;
-    for (int32_t j0 = 0; j0 < n; j0 += kChoose) {
-        const int32_t j = j0 + threadIdx.x;
-        const float x = j < n ? scores[j] : 0.f;
-        const bool decided = j >= lo && j < hi;
-        const uint32_t o = order_of(x);
-        const bool equal = decided && wanted > 0 && o == prefix;
-        int total;
-        const int rank = equals + block_prefix(equal, warp_sums, total);
-        equals += total;
-        const bool stays = j < n && (!decided || (wanted > 0 && (o > prefix || (equal && rank < left))));
-        const int place = at + block_prefix(stays, warp_sums, total);
-        at += total;
-        if (stays) {
-            kept[place] = j;
-            if (out) out[place] = x;
+    int32_t *kept = a.kept + b * budget;
+    float *out = a.scores_out ? a.scores_out + b * budget : nullptr;
+    for (uint32_t j0 = slice0; j0 < slice1; j0 += tile) {
+        const uint32_t first = j0 + warp * share + lane;
+        uint32_t is_sure = 0, is_tied = 0;       // bit k: this lane's row of round k
+        int n_sure = 0, n_tied = 0;
+        for (int k0 = 0; k0 < rounds; k0 += 8) {
+            float x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t j = first + 32 * (k0 + i);
+                x[i] = k0 + i < rounds && j < slice1 ? scores[j] : 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t j = first + 32 * (k0 + i);
+                const bool there = k0 + i < rounds && j < slice1, decided = j >= lo && j < hi;
+                const uint32_t o = order_of(x[i]);
+                const bool s = there && (!decided || (wanted > 0 && o > prefix));
+                const bool t = there && decided && wanted > 0 && o == prefix;
+                is_sure |= (uint32_t)s << (k0 + i);
+                is_tied |= (uint32_t)t << (k0 + i);
+                n_sure += __popc(__ballot_sync(0xffffffffu, s));
+                n_tied += __popc(__ballot_sync(0xffffffffu, t));
+            }
         }
+        __syncthreads();
+        if (lane == 0) more[0][warp] = n_sure, more[1][warp] = n_tied;
+        __syncthreads();
+        int w_sure = lane < warp ? more[0][lane] : 0, w_tied = lane < warp ? more[1][lane] : 0;
+        int t_sure = more[0][lane], t_tied = more[1][lane];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            w_sure += __shfl_xor_sync(0xffffffffu, w_sure, o);
+            w_tied += __shfl_xor_sync(0xffffffffu, w_tied, o);
+            t_sure += __shfl_xor_sync(0xffffffffu, t_sure, o);
+            t_tied += __shfl_xor_sync(0xffffffffu, t_tied, o);
+        }
+        int g = sure + w_sure, e = tied + w_tied;
+        for (int k = 0; k < rounds; ++k) {
+            const bool s = is_sure >> k & 1, t = is_tied >> k & 1;
+            const uint32_t bs = __ballot_sync(0xffffffffu, s), bt = __ballot_sync(0xffffffffu, t);
+            const uint32_t below = (1u << lane) - 1;
+            const int before = e + __popc(bt & below);
+            if (s || (t && before < left)) {
+                const int place = g + __popc(bs & below) + min(before, left);
+                const uint32_t j = first + 32 * k;
+                kept[place] = (int32_t)j;
+                if (out) out[place] = scores[j];
+            }
+            g += __popc(bs);
+            e += __popc(bt);
+        }
+        sure += t_sure;
+        tied += t_tied;
     }
-    for (int32_t j = stay + threadIdx.x; j < a.budget; j += kChoose) {
+    for (uint32_t j = stay + rank * kChoose + threadIdx.x; j < budget; j += CS * kChoose) {
         kept[j] = -1;
         if (out) out[j] = 0.f;
     }
-    if (threadIdx.x == 0) a.lengths[b] = stay;
+    if (threadIdx.x == 0 && rank == 0) a.lengths[b] = (int32_t)stay;
+    if (CS > 1) cluster.sync();           // the others may still read this block's counts
 }
 
-__global__ void __launch_bounds__(256) evict_copy(EvictArgs a) {
+constexpr int kCopy = 256, kCopyRows = 2, kCopyChunks = 4;
+
+// Threads that share a row of so many 16-byte chunks: a power of two, about four chunks each.
+__host__ __device__ inline uint32_t row_threads(uint32_t chunks) {
+    uint32_t n = 1;
+    while (n < 32 && n * kCopyChunks < chunks) n *= 2;
+    return n;
+}
+
+// Copies a sequence's kept rows of one cache; grid (groups of rows, caches, sequences). A thread has
+// two rows on the way at once, four chunks of each.
+__global__ void __launch_bounds__(kCopy) evict_copy(EvictArgs a) {
+    await_previous();
     const slikl_evict_cache &c = a.caches[blockIdx.y];
-    const int64_t chunks = c.row_bytes / 16, total = a.B * a.budget * chunks;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total;
-         i += (int64_t)gridDim.x * 256) {
-        const int64_t row = i / chunks, part = i - row * chunks, b = row / a.budget;
-        const int32_t j = a.kept[row];
-        if (j < 0) continue;
+    const uint32_t chunks = (uint32_t)(c.row_bytes / 16), tpr = row_threads(chunks);
+    const uint32_t col = threadIdx.x & (tpr - 1), mine = threadIdx.x / tpr, across = kCopy / tpr;
+    for (int64_t b = blockIdx.z; b < a.B; b += gridDim.z) {
+        const int32_t *kept = a.kept + b * a.budget;
         const int64_t base = a.layout_k == SLIKL_BSND ? b * a.S2 : a.cu_k[b];
-        static_cast<uint4 *>(c.out)[row * chunks + part] =
-            static_cast<const uint4 *>(c.in)[(base + j) * chunks + part];
+        const uint4 *in = static_cast<const uint4 *>(c.in) + base * chunks;
+        uint4 *out = static_cast<uint4 *>(c.out) + b * a.budget * chunks;
+        for (uint32_t row = blockIdx.x * across * kCopyRows + mine; row < (uint32_t)a.budget;
+             row += gridDim.x * across * kCopyRows) {
+            const uint32_t next = row + across;
+            const int32_t j0 = kept[row], j1 = next < (uint32_t)a.budget ? kept[next] : -1;
+            const uint4 *p0 = in + (int64_t)j0 * chunks, *p1 = in + (int64_t)j1 * chunks;
+            uint4 *q0 = out + (int64_t)row * chunks, *q1 = out + (int64_t)next * chunks;
+            for (uint32_t k = col; k < chunks; k += kCopyChunks * tpr) {
+                uint4 v0[kCopyChunks], v1[kCopyChunks];
+#pragma unroll
+                for (int i = 0; i < kCopyChunks; ++i) {
+                    if (j0 >= 0 && k + i * tpr < chunks) v0[i] = p0[k + i * tpr];
+                    if (j1 >= 0 && k + i * tpr < chunks) v1[i] = p1[k + i * tpr];
+                }
+#pragma unroll
+                for (int i = 0; i < kCopyChunks; ++i) {
+                    if (j0 >= 0 && k + i * tpr < chunks) q0[k + i * tpr] = v0[i];
+                    if (j1 >= 0 && k + i * tpr < chunks) q1[k + i * tpr] = v1[i];
+                }
+            }
+        }
     }
 }
 
@@ -189,7 +313,7 @@ slikl_status slikl_evict(const slikl_evict_problem *problem, const slikl_evict_t
     const slikl_evict_problem &p = *problem;
     const int64_t limit = int64_t(1) << 31;
     if ((p.layout_k != SLIKL_BSND && p.layout_k != SLIKL_TND) || p.n_caches < 0 ||
-        p.n_caches > SLIKL_EVICT_MAX_CACHES || p.B < 1 || p.B >= limit || p.budget < 1 ||
+        p.n_caches > SLIKL_EVICT_MAX_CACHES || p.B < 1 || p.B >= limit / 8 || p.budget < 1 ||
         p.budget >= limit || p.B * p.budget >= limit || p.sinks < 0 || p.recent < 0 ||
         p.sinks > p.budget || p.recent > p.budget - p.sinks)
         return SLIKL_ERR_PARAM_INVALID;
@@ -251,19 +375,22 @@ slikl_status slikl_evict(const slikl_evict_problem *problem, const slikl_evict_t
     a.lengths = t.lengths;
     a.scores_out = t.scores_out;
     a.status = t.status;
-    int64_t most = 0;
+    int64_t blocks = 0;
     for (int i = 0; i < p.n_caches; ++i) {
         a.caches[i] = t.caches[i];
-        most = most > t.caches[i].row_bytes ? most : t.caches[i].row_bytes;
+        const int64_t rows = kCopyRows * (kCopy / row_threads((uint32_t)(t.caches[i].row_bytes / 16)));
+        blocks = std::max(blocks, (p.budget + rows - 1) / rows);
     }
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    evict_choose<<<(unsigned)p.B, kChoose, 0, s>>>(a);
+    // Sequences of up to 8192 rows, eight a thread, go through one block faster than through a
+    // cluster, whose barriers cost more than they share out.
+    const int64_t range = p.layout_k == SLIKL_BSND ? p.S2 : p.S2 > 0 ? std::min(p.S2, T2) : T2;
+    if (range <= 8192) evict_choose<1><<<(unsigned)p.B, kChoose, 0, s>>>(a);
+    else evict_choose<8><<<(unsigned)p.B * 8, kChoose, 0, s>>>(a);
     if (cudaGetLastError() != cudaSuccess) return SLIKL_ERR_CUDA;
     if (p.n_caches > 0) {
-        const int64_t blocks = (places * (most / 16) + 255) / 256;
-        evict_copy<<<dim3((unsigned)(blocks < 148 * 16 ? blocks : 148 * 16), (unsigned)p.n_caches),
-                     256, 0, s>>>(a);
-        if (cudaGetLastError() != cudaSuccess) return SLIKL_ERR_CUDA;
+        const dim3 grid((unsigned)blocks, (unsigned)p.n_caches, (unsigned)std::min<int64_t>(p.B, 65535));
+        if (launch_next(evict_copy, grid, kCopy, s, a) != cudaSuccess) return SLIKL_ERR_CUDA;
     }
     return SLIKL_OK;
 }

@@ -403,9 +403,10 @@ slikl_status slikl_key_weights(const slikl_problem *problem,
             if (cudaGetLastError() != cudaSuccess) return SLIKL_ERR_CUDA;
         }
     }
-    return launch_next(weights_finish, dim3((unsigned)((T2 + 255) / 256)), 256, s, a) == cudaSuccess
-               ? SLIKL_OK
-               : SLIKL_ERR_CUDA;
+    const dim3 grid((unsigned)((T2 + 255) / 256));
+    if (T1 > 0) return launch_next(weights_finish, grid, 256, s, a) == cudaSuccess ? SLIKL_OK : SLIKL_ERR_CUDA;
+    weights_finish<<<grid, 256, 0, s>>>(a);
+    return cudaGetLastError() == cudaSuccess ? SLIKL_OK : SLIKL_ERR_CUDA;
 }
 
 }  // extern "C"
