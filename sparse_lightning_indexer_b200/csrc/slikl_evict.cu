@@ -89,13 +89,16 @@ __device__ int block_prefix(int v, int *warp_sums) {
     return x - v + warp_sums[warp];
 }
 
-// Rows [j0, j0 + 32 * rounds) of a warp's share, a round 32 neighbours; at most kRounds rounds a tile.
-constexpr int kRounds = 16;
-
-template <int CS>
+// CS blocks share a sequence; a tile of a block's slice is ROUNDS rows for each of its threads, which hold
+// their order numbers in registers: row 32 k of a warp's share (32 ROUNDS neighbours) and the lane's place.
+// The usual slice is one tile, read once; a longer one is read again for every pass.
+template <int CS, int ROUNDS>
 __global__ void __launch_bounds__(kChoose) __cluster_dims__(CS, 1, 1) evict_choose(EvictArgs a) {
     namespace cg = cooperative_groups;
-    __shared__ int bins[3][kBins];       // of each pass: the other blocks may still read an earlier one
+    constexpr bool SMALL = CS == 1 && ROUNDS == 1;
+    constexpr uint32_t SHARE = 32 * ROUNDS, TILE = kChoose * ROUNDS;
+    __shared__ int bins[SMALL ? 1 : 3][SMALL ? 1 : kBins];   // of each pass: the other blocks may still
+                                                             // read an earlier one
     __shared__ int warp_sums[32], more[2][32];
     __shared__ uint32_t found_bin;
     __shared__ int found_above, counts[2];
@@ -110,37 +113,54 @@ __global__ void __launch_bounds__(kChoose) __cluster_dims__(CS, 1, 1) evict_choo
     const uint32_t lo = all ? 0 : a.sinks, hi = all ? 0 : n - a.recent;   // rows that scores decide on
     const uint32_t wanted = all ? 0 : budget - a.sinks - a.recent;
     const float *scores = a.scores + q.base;
-    // the block's slice of the rows, and its warps' shares of a tile of it
     const uint32_t per = (n + CS - 1) / CS, slice0 = min(n, rank * per), slice1 = min(n, slice0 + per);
-    const int rounds = min((slice1 - slice0 + kChoose - 1) / kChoose, (uint32_t)kRounds);
-    const uint32_t share = 32 * rounds, tile = 32 * share;
+    const bool once = slice1 - slice0 <= TILE;
+    const uint32_t first = slice0 + warp * SHARE + lane;     // the thread's first row of the first tile
+
+    uint32_t order[ROUNDS], decided = 0;      // bit k: row k is one that scores decide on
+    auto read_tile = [&](uint32_t j) {
+        decided = 0;
+        float x[ROUNDS];
+#pragma unroll
+        for (int k = 0; k < ROUNDS; ++k)          // (all on the way at once: no load behind a branch)
+            x[k] = scores[min(j + 32 * k, slice1 - 1)];
+#pragma unroll
+        for (int k = 0; k < ROUNDS; ++k) {
+            order[k] = order_of(x[k]);
+            decided |= (uint32_t)(j + 32 * k >= lo && j + 32 * k < min(hi, slice1)) << k;
+        }
+    };
+    if (slice0 < slice1) read_tile(first);
 
     // the order number of the wanted-th of them, and how many rows with that number stay
-    uint32_t prefix = 0, mask = 0;
+    uint32_t prefix = 0;
     int left = wanted, above_mine = 0;
-    if (wanted > 0) {
+    if (wanted > 0 && SMALL && once) {
+        // a row a thread: the number bit by bit, a barrier that counts for each
+        for (int bit = 31; bit >= 0; --bit) {
+            const uint32_t next = prefix | 1u << bit;
+            if (__syncthreads_count(decided && order[0] >= next) >= (int)wanted) prefix = next;
+        }
+        left -= __syncthreads_count(decided && order[0] > prefix);
+    } else if (wanted > 0 && !SMALL) {
+        uint32_t mask = 0;
         for (int i = threadIdx.x; i < 3 * kBins; i += kChoose) bins[0][i] = 0;
         __syncthreads();
         for (int pass = 0; pass < 3; ++pass) {
             const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, width = pass == 2 ? 10 : 11;
-            // (eight loads on the way at once)
-            const uint32_t end = min(hi, slice1);
-            for (uint32_t j = max(lo, slice0) + threadIdx.x; j < end; j += 8 * kChoose) {
-                float x[8];
+            for (uint32_t j = 0; j < slice1 - slice0; j += TILE) {
+                if (!once) read_tile(first + j);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = j + i * kChoose < end ? scores[j + i * kChoose] : 0.f;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const uint32_t o = order_of(x[i]);
-                    if (j + i * kChoose < end && (o & mask) == prefix)
-                        atomicAdd(&bins[pass][(o >> shift) & ((1u << width) - 1)], 1);
-                }
+                for (int k = 0; k < ROUNDS; ++k)
+                    if ((decided >> k & 1) && (order[k] & mask) == prefix)
+                        atomicAdd(&bins[pass][(order[k] >> shift) & ((1u << width) - 1)], 1);
             }
             if (CS == 1) __syncthreads();
             else cluster.sync();
             // thread i holds bins 2047 - 2i and 2046 - 2i: the prefix runs from the highest bin
             const int bin = kBins - 2 - 2 * threadIdx.x;
-            int h1 = 0, h0 = 0, m1 = bins[pass][bin], m0 = bins[pass][bin + 1];
+            const int m1 = bins[pass][bin], m0 = bins[pass][bin + 1];
+            int h1 = 0, h0 = 0;
             if (CS == 1) {
                 h1 = m1, h0 = m0;
             } else {
@@ -152,9 +172,9 @@ __global__ void __launch_bounds__(kChoose) __cluster_dims__(CS, 1, 1) evict_choo
             }
             const int above = block_prefix(h0 + h1, warp_sums);
             if (above < left && left <= above + h0 + h1) {
-                const bool first = left <= above + h0;
-                found_bin = bin + (first ? 1 : 0);
-                found_above = above + (first ? 0 : h0);
+                const bool upper = left <= above + h0;
+                found_bin = bin + (upper ? 1 : 0);
+                found_above = above + (upper ? 0 : h0);
             }
             __syncthreads();
             const int found = found_bin;
@@ -173,7 +193,7 @@ __global__ void __launch_bounds__(kChoose) __cluster_dims__(CS, 1, 1) evict_choo
             const uint32_t from = max(lo, slice0), to = min(hi, slice1);
             const uint32_t inside = from < to ? to - from : 0;
             counts[0] = total + (int)(slice1 - slice0 - inside);
-            counts[1] = wanted > 0 ? bins[2][prefix & 1023] : 0;
+            counts[1] = wanted > 0 ? bins[SMALL ? 0 : 2][SMALL ? 0 : prefix & 1023] : 0;
         }
         cluster.sync();
         for (int r = 0; r < (int)rank; ++r) {
@@ -185,29 +205,20 @@ __global__ void __launch_bounds__(kChoose) __cluster_dims__(CS, 1, 1) evict_choo
 
     int32_t *kept = a.kept + b * budget;
     float *out = a.scores_out ? a.scores_out + b * budget : nullptr;
-    for (uint32_t j0 = slice0; j0 < slice1; j0 += tile) {
-        const uint32_t first = j0 + warp * share + lane;
+    for (uint32_t j0 = 0; j0 < slice1 - slice0; j0 += TILE) {
+        if (!once) read_tile(first + j0);
         uint32_t is_sure = 0, is_tied = 0;       // bit k: this lane's row of round k
         int n_sure = 0, n_tied = 0;
-        for (int k0 = 0; k0 < rounds; k0 += 8) {
-            float x[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint32_t j = first + 32 * (k0 + i);
-                x[i] = k0 + i < rounds && j < slice1 ? scores[j] : 0.f;
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint32_t j = first + 32 * (k0 + i);
-                const bool there = k0 + i < rounds && j < slice1, decided = j >= lo && j < hi;
-                const uint32_t o = order_of(x[i]);
-                const bool s = there && (!decided || (wanted > 0 && o > prefix));
-                const bool t = there && decided && wanted > 0 && o == prefix;
-                is_sure |= (uint32_t)s << (k0 + i);
-                is_tied |= (uint32_t)t << (k0 + i);
-                n_sure += __popc(__ballot_sync(0xffffffffu, s));
-                n_tied += __popc(__ballot_sync(0xffffffffu, t));
-            }
+        for (int k = 0; k < ROUNDS; ++k) {
+            const bool d = decided >> k & 1;
+            const bool s = d ? wanted > 0 && order[k] > prefix : first + j0 + 32 * k < slice1 &&
+                               !(first + j0 + 32 * k >= lo && first + j0 + 32 * k < hi);
+            const bool t = d && wanted > 0 && order[k] == prefix;
+            is_sure |= (uint32_t)s << k;
+            is_tied |= (uint32_t)t << k;
+            n_sure += __popc(__ballot_sync(0xffffffffu, s));
+            n_tied += __popc(__ballot_sync(0xffffffffu, t));
         }
         __syncthreads();
         if (lane == 0) more[0][warp] = n_sure, more[1][warp] = n_tied;
@@ -222,14 +233,15 @@ __global__ void __launch_bounds__(kChoose) __cluster_dims__(CS, 1, 1) evict_choo
             t_tied += __shfl_xor_sync(0xffffffffu, t_tied, o);
         }
         int g = sure + w_sure, e = tied + w_tied;
-        for (int k = 0; k < rounds; ++k) {
+        // (no loop for warps that keep nothing)
+        for (int k = 0; k < (n_sure + n_tied ? ROUNDS : 0); ++k) {
             const bool s = is_sure >> k & 1, t = is_tied >> k & 1;
             const uint32_t bs = __ballot_sync(0xffffffffu, s), bt = __ballot_sync(0xffffffffu, t);
             const uint32_t below = (1u << lane) - 1;
             const int before = e + __popc(bt & below);
             if (s || (t && before < left)) {
                 const int place = g + __popc(bs & below) + min(before, left);
-                const uint32_t j = first + 32 * k;
+                const uint32_t j = first + j0 + 32 * k;
                 kept[place] = (int32_t)j;
                 if (out) out[place] = scores[j];
             }
@@ -382,11 +394,14 @@ slikl_status slikl_evict(const slikl_evict_problem *problem, const slikl_evict_t
         blocks = std::max(blocks, (p.budget + rows - 1) / rows);
     }
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    // Sequences of up to 8192 rows, eight a thread, go through one block faster than through a
-    // cluster, whose barriers cost more than they share out.
+    // Sequences of up to 8192 rows, eight a thread, go through one block: a cluster's barriers cost more
+    // than they share out. (The one-row form is right for a length that breaks the promise only with
+    // its passes, which it lacks: it is for lengths that the tensors themselves bound.)
     const int64_t range = p.layout_k == SLIKL_BSND ? p.S2 : p.S2 > 0 ? std::min(p.S2, T2) : T2;
-    if (range <= 8192) evict_choose<1><<<(unsigned)p.B, kChoose, 0, s>>>(a);
-    else evict_choose<8><<<(unsigned)p.B * 8, kChoose, 0, s>>>(a);
+    const int64_t bound = p.layout_k == SLIKL_BSND ? p.S2 : T2;
+    if (bound <= kChoose) evict_choose<1, 1><<<(unsigned)p.B, kChoose, 0, s>>>(a);
+    else if (range <= 8192) evict_choose<1, 8><<<(unsigned)p.B, kChoose, 0, s>>>(a);
+    else evict_choose<8, 16><<<(unsigned)p.B * 8, kChoose, 0, s>>>(a);
     if (cudaGetLastError() != cudaSuccess) return SLIKL_ERR_CUDA;
     if (p.n_caches > 0) {
         const dim3 grid((unsigned)blocks, (unsigned)p.n_caches, (unsigned)std::min<int64_t>(p.B, 65535));

@@ -12,7 +12,7 @@
 //   weights_direct  few slots a batch (a decoding step): a block owns a chunk of a batch's keys, reads
 //                   all of the batch's slots, keeps both words and writes the chunk's result: one
 //                   launch and no workspace;
-//   weights_split   else: blocks share a batch's slots, keep the low words of up to 55296 keys (larger
+//   weights_split   else: blocks share a batch's slots, keep the low words of up to 45056 keys (larger
 //                   ranges are covered by several blocks that read the same slots, from L2 mostly)
 //                   and add them to 64-bit sums in the workspace once; weights_finish makes the result.
 #include <algorithm>
@@ -73,112 +73,98 @@ __device__ Batch batch_of(const WeightArgs &a, int64_t b) {
     return r;
 }
 
-// A weight in units of 2^-u.
-__device__ __forceinline__ uint64_t units(const WeightArgs &a, float w) {
-    if (!(w >= 0.f && w <= 2.f)) {
+// A weight, times 2^u in fp32 (exact), as an integer; bad ones are flagged and cut to [0, 2].
+__device__ __forceinline__ uint64_t units(const WeightArgs &a, float x) {
+    if (!(x >= 0.f && x <= 2.f * a.one)) {
         flag(a, SLIKL_DEV_BAD_WEIGHT);
-        w = w > 2.f ? 2.f : 0.f;
+        x = x > 0.f ? 2.f * a.one : 0.f;
     }
-    return (uint64_t)__float2ll_rn(w * a.one);
+    return (uint64_t)__float2ll_rn(x);
 }
 
-// Adds n to the shared word at `at` and returns what was there; 0 where `take` is false.
-__device__ __forceinline__ uint32_t add_low(uint32_t at, uint32_t n, bool take = true) {
-    uint32_t was = 0;
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %3, 0;\n\t"
-                 "@p atom.shared.add.u32 %0, [%1], %2;\n\t}"
-                 : "+r"(was)
-                 : "r"(at), "r"(n), "r"((uint32_t)take)
-                 : "memory");
-    return was;
+// Four slots a thread, v their keys in the chunk (at least `named` where a slot does not count) and w
+// their weights: added to the low words. Of the 32 words behind the chunk, the lane's takes what does
+// not count, as zero, so that the usual step has no branch. more(key, n) adds n times 2^32. Weights of
+// 2^(32-u) and more, bad ones and carries are seen to behind the additions.
+template <typename F>
+__device__ __forceinline__ void add_four(const WeightArgs &a, const uint32_t *v, const float *w,
+                                         uint32_t named, uint32_t keys, uint32_t *low, const F &more) {
+    const uint32_t small = __float_as_uint(4294967296.f);     // bits of 0 <= x < 2^32 are below
+    float x[4];
+    const uint32_t spare = keys + (threadIdx.x & 31);
+    uint32_t most = 0, carries = 0;
+    bool some = false;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) some |= v[k] < named;
+    // (rows are sorted more often than not, and all of a warp's slots outside the chunk then)
+    if (!__any_sync(0xffffffffu, some)) return;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        x[k] = v[k] < named ? w[k] * a.one : 0.f;
+        most = max(most, __float_as_uint(x[k]));
+    }
+    if (most < small) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t lo = __float2uint_rn(x[k]);
+            carries |= (uint32_t)(atomicAdd(low + (v[k] < named ? v[k] : spare), lo) > ~lo) << k;
+        }
+        if (!carries) return;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        if (v[k] >= named || (most < small && !(carries >> k & 1))) continue;
+        uint32_t hi = 1;
+        if (most >= small) {
+            const uint64_t u = units(a, x[k]);
+            const uint32_t lo = (uint32_t)u;
+            hi = (uint32_t)(u >> 32) + (atomicAdd(low + v[k], lo) > ~lo);
+        }
+        if (hi) more(v[k], hi);
+    }
 }
 
-// Adds the weights of the slots of [begin, end) that name a key of [first, first + keys) to the low
-// words; more(key, n) adds n times 2^32. Flags indices that break the contract.
-//
-// A thread takes kAtOnce slots at a time, a block's width apart: neighbouring threads hold neighbouring
-// slots, whose keys, where a row is sorted, meet in few banks. Loads run ahead: the indices two such
-// steps, the weights (read only where the slot counts) one, since their latency was what the plain
-// loop spent its time on. Carries, weights of 2^(32-u) and more and bad ones are seen to behind the
-// step's additions, together.
-constexpr int kAtOnce = 4;
-
+// Adds the slots of [begin, end) that name a key of [first, first + keys) to the low words. Flags
+// indices that break the contract. A step is four slots a thread, a block's width apart; loads run
+// ahead, the indices two steps and the weights, read only where the slot counts, one.
 template <int THREADS, typename F>
-__device__ __forceinline__ void add_slots(const WeightArgs &a, const Batch &r, int64_t begin,
-                                          int64_t end, int32_t first, int32_t keys, uint32_t *low,
-                                          F more) {
-    constexpr int N = kAtOnce;
-    constexpr uint32_t STEP = N * THREADS;
-    const uint32_t named = (uint32_t)max(0, min(keys, r.used - first)), count = r.count;
-    const uint32_t slots = (uint32_t)(end - begin), at = (uint32_t)__cvta_generic_to_shared(low);
+__device__ __forceinline__ void add_some(const WeightArgs &a, const Batch &r, int64_t begin, int64_t end,
+                                         int32_t first, int32_t keys, uint32_t *low, const F &more) {
+    constexpr uint32_t STEP = 4 * THREADS;
+    const uint32_t named = (uint32_t)max(0, min(keys, r.used - first));
+    const uint32_t slots = (uint32_t)(end - begin);
     const int32_t *idx = a.idx + begin;
     const float *weights = a.weights + begin;
-    const uint32_t small = __float_as_uint(4294967296.f);     // bits of 0 <= x < 2^32 are below
     uint32_t largest = 0;     // of the indices plus one
-    // (indices as keys of the chunk: those outside it are at least `named`)
     auto indices = [&](uint32_t i, uint32_t *v) {
         const int32_t *p = idx + i;
-        if (i + (N - 1) * THREADS < slots) {
 #pragma unroll
-            for (int k = 0; k < N; ++k) v[k] = p[k * THREADS];
-        } else {
-#pragma unroll
-            for (int k = 0; k < N; ++k) v[k] = i + k * THREADS < slots ? p[k * THREADS] : -1;
-        }
+        for (int k = 0; k < 4; ++k) v[k] = i + k * THREADS < slots ? p[k * THREADS] : -1;
     };
-    auto scaled = [&](uint32_t i, uint32_t *v, float *w) {
+    auto load = [&](uint32_t i, uint32_t *v, float *w) {
         const float *p = weights + i;
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
+        for (int k = 0; k < 4; ++k) {
             largest = max(largest, v[k] + 1);
             v[k] -= first;
             w[k] = v[k] < named ? p[k * THREADS] : 0.f;
         }
     };
-    auto add = [&](const uint32_t *v, const float *w) {
-        // (rows are sorted more often than not, and all of a warp's slots outside the chunk then)
-        bool some = false;
-#pragma unroll
-        for (int k = 0; k < N; ++k) some |= v[k] < named;
-        if (!__any_sync(0xffffffffu, some)) return;
-        uint32_t rare = 0;
-#pragma unroll
-        for (int k = 0; k < N; ++k) {
-            const float x = w[k] * a.one;
-            const bool odd = __float_as_uint(x) >= small;
-            const uint32_t lo = __float2uint_rn(x);
-            const uint32_t was = add_low(at + 4 * v[k], lo, v[k] < named && !odd);
-            if (odd || was > ~lo) rare |= 1u << k;           // ... or a carry
-        }
-        if (!rare) return;
-#pragma unroll
-        for (int k = 0; k < N; ++k) {
-            if (!(rare >> k & 1) || v[k] >= named) continue;
-            uint32_t hi = 1;
-            if (__float_as_uint(w[k] * a.one) >= small) {
-                const uint64_t u = units(a, w[k]);
-                const uint32_t lo = (uint32_t)u;
-                hi = (uint32_t)(u >> 32) + (add_low(at + 4 * v[k], lo) > ~lo);
-            }
-            if (hi) more(v[k], hi);
-        }
-    };
-    uint32_t v[3][N];
-    float w[2][N];
-    uint32_t i = threadIdx.x;
+    uint32_t v[3][4], i = threadIdx.x;
+    float w[2][4];
     indices(i, v[0]);
     indices(i + STEP, v[1]);
-    scaled(i, v[0], w[0]);
+    load(i, v[0], w[0]);
     for (uint32_t all = 0; all < slots; all += 6 * STEP, i += 6 * STEP) {   // the same steps for all threads
 #pragma unroll
         for (int j = 0; j < 6; ++j) {
             if (j && all + j * STEP >= slots) break;
             indices(i + (j + 2) * STEP, v[(j + 2) % 3]);
-            scaled(i + (j + 1) * STEP, v[(j + 1) % 3], w[(j + 1) % 2]);
-            add(v[j % 3], w[j % 2]);
+            load(i + (j + 1) * STEP, v[(j + 1) % 3], w[(j + 1) % 2]);
+            add_four(a, v[j % 3], w[j % 2], named, keys, low, more);
         }
     }
-    if (largest > count) flag(a, SLIKL_DEV_INDEX_OUT_OF_RANGE);
+    if (largest > (uint32_t)r.count) flag(a, SLIKL_DEV_INDEX_OUT_OF_RANGE);
 }
 
 // What the per-batch arrays promise, looked at once by the first block of weights_finish.
@@ -215,7 +201,7 @@ constexpr int kSplitThreads = 1024, kSplitKeys = 55296;       // 216 KB of low w
 
 // grid (chunks of keys, batches).
 __global__ void __launch_bounds__(kDirectThreads) weights_direct(WeightArgs a, int chunk) {
-    __shared__ uint32_t low[kDirectKeys], high[kDirectKeys];
+    __shared__ uint32_t low[kDirectKeys + 32], high[kDirectKeys];
     const int64_t b = blockIdx.y;
     if (blockIdx.x == 0 && b == 0 && a.status) check_batches(a);
     const Batch r = batch_of(a, b);
@@ -224,8 +210,8 @@ __global__ void __launch_bounds__(kDirectThreads) weights_direct(WeightArgs a, i
         const int32_t keys = (int32_t)min((int64_t)chunk, r.count - first);
         for (int i = threadIdx.x; i < keys; i += kDirectThreads) low[i] = high[i] = 0;
         __syncthreads();
-        add_slots<kDirectThreads>(a, r, r.begin, r.end, (int32_t)first, keys, low,
-                  [&](int32_t k, uint32_t n) { atomicAdd(&high[k], n); });
+        add_some<kDirectThreads>(a, r, r.begin, r.end, (int32_t)first, keys, low,
+                                 [&](uint32_t k, uint32_t n) { atomicAdd(&high[k], n); });
         __syncthreads();
         for (int i = threadIdx.x; i < keys; i += kDirectThreads) {
             const int64_t key = r.base + first + i;
@@ -241,8 +227,10 @@ __global__ void __launch_bounds__(kSplitThreads) weights_split(WeightArgs a, int
     let_next_start();         // weights_finish
     const Batch r = batch_of(a, a.first_batch + blockIdx.z);
     const int64_t slots = r.end - r.begin;
-    const int64_t begin = r.begin + slots * blockIdx.y / gridDim.y;
-    const int64_t end = r.begin + slots * (blockIdx.y + 1) / gridDim.y;
+    // (shares of whole fours, so that they are aligned alike)
+    const int64_t begin = r.begin + ((slots * blockIdx.y / gridDim.y) & ~(int64_t)3);
+    const int64_t end = blockIdx.y + 1 == gridDim.y ? r.end
+                                                    : r.begin + ((slots * (blockIdx.y + 1) / gridDim.y) & ~(int64_t)3);
     if (begin == end) return;
     for (int64_t first = (int64_t)blockIdx.x * chunk; first < r.used;
          first += (int64_t)gridDim.x * chunk) {
@@ -250,9 +238,8 @@ __global__ void __launch_bounds__(kSplitThreads) weights_split(WeightArgs a, int
         unsigned long long *sums = a.sums + r.base + first;
         for (int i = threadIdx.x; i < keys; i += kSplitThreads) low[i] = 0;
         __syncthreads();
-        add_slots<kSplitThreads>(a, r, begin, end, (int32_t)first, keys, low, [&](int32_t k, uint32_t n) {
-            atomicAdd(sums + k, (unsigned long long)n << 32);
-        });
+        const auto more = [&](uint32_t k, uint32_t n) { atomicAdd(sums + k, (unsigned long long)n << 32); };
+        add_some<kSplitThreads>(a, r, begin, end, (int32_t)first, keys, low, more);
         __syncthreads();
         for (int i = threadIdx.x; i < keys; i += kSplitThreads)
             if (low[i]) atomicAdd(sums + i, (unsigned long long)low[i]);
@@ -386,20 +373,19 @@ slikl_status slikl_key_weights(const slikl_problem *problem,
     if (T1 > 0) {
         const int64_t chunks = (range + kSplitKeys - 1) / kSplitKeys;
         const int64_t chunk = (range + chunks - 1) / chunks;
-        const size_t smem = sizeof(uint32_t) * (size_t)chunk;
+        const size_t smem = sizeof(uint32_t) * (size_t)(chunk + 32);
         // as many splits as fill the multiprocessors, each of 4096 slots at least
-        const int64_t per_sm = smem > 100 * 1024 ? 1 : 2;
-        const int64_t splits = std::max<int64_t>(
-            1, std::min(sms * per_sm / (chunks * pr.B), (T1 * pr.topk / pr.B + 4095) / 4096));
+        const int64_t splits =
+            std::max<int64_t>(1, std::min(sms / (chunks * pr.B), (T1 * pr.topk / pr.B + 4095) / 4096));
         if (cudaFuncSetAttribute(weights_split, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)(sizeof(uint32_t) * kSplitKeys)) != cudaSuccess)
+                                 (int)(sizeof(uint32_t) * (kSplitKeys + 32))) != cudaSuccess)
             return SLIKL_ERR_CUDA;
         WeightArgs part = a;
         // the grid's third dimension holds 65535 batches
         for (int64_t b = 0; b < pr.B; b += 65535) {
             part.first_batch = b;
             weights_split<<<dim3((unsigned)chunks, (unsigned)splits, (unsigned)std::min<int64_t>(pr.B - b, 65535)),
-                            kSplitThreads, smem, s>>>(part, (int)chunk);
+                     kSplitThreads, smem, s>>>(part, (int)chunk);
             if (cudaGetLastError() != cudaSuccess) return SLIKL_ERR_CUDA;
         }
     }
