@@ -968,11 +968,13 @@ int sm100_multiprocessors() {
     return ok && major == 10 ? sms : 0;
 }
 
-// Blocks of both sides, `most` at most, in proportion to the instructions that their rows take; a
-// side with rows gets one at least. (Counted on B200: a row of a token with few heads takes 1.6 times
-// as many as one of 64 heads, whose angles are ready, a layer norm 1.25 times an RMS norm's.) A
-// small call gets a group of rows for each warp, so that it spreads over all multiprocessors.
-void share_blocks(Args &a, int64_t D, int sms, int per_sm) {
+// Blocks of both sides, as many as the multiprocessors hold, in proportion to what their rows take; a
+// side with rows gets one at least. A row of a token with few heads, for which angles come from the
+// table, takes 1 + few / N times as long as one of many heads (measured over shares on B200: with
+// few = 0.6 the varlen forward took 122 us, with 3 110; the gradient at the checkpoint 94 with 0.6,
+// 84 with 1.1 and 2, 88 with 3), and a layer norm 1.25 times as long as an RMS norm. A small call gets
+// a group of rows for each warp, so that it spreads over all multiprocessors.
+void share_blocks(Args &a, int64_t D, int sms, int per_sm, double few) {
     const uint32_t most = (uint32_t)(std::min(sms, kMaxSms) * per_sm), warps = kThreads / 32;
     const uint32_t rpw = (uint32_t)(512 / D);
     uint32_t groups[2], blocks[2];
@@ -984,7 +986,7 @@ void share_blocks(Args &a, int64_t D, int sms, int per_sm) {
         const uint32_t per = rpw << s.two;
         groups[i] = (s.rows + per - 1) / per;
         blocks[i] = (groups[i] + warps - 1) / warps;
-        cost[i] = s.rows * (1.0 + 0.6 / s.N.d) * (s.norm == SLIKL_NORM_LAYER ? 1.25 : 1.0);
+        cost[i] = s.rows * (s.two ? 1.0 : 1.0 + few / s.N.d) * (s.norm == SLIKL_NORM_LAYER ? 1.25 : 1.0);
     }
     if ((uint64_t)blocks[0] + blocks[1] > most) {
         const uint32_t share = (uint32_t)(most * (cost[1] / (cost[0] + cost[1])) + 0.5);
@@ -1023,7 +1025,7 @@ Kernel pick(const slikl_qk_problem &p, const K &k) {
 slikl_status run_forward(const slikl_qk_problem *p, const slikl_qk_tensors *t, int sms,
                          cudaStream_t st) {
     Args a = make_args(p, t);
-    share_blocks(a, p->D, sms, kFwdPerSm);
+    share_blocks(a, p->D, sms, kFwdPerSm, 3.0);
     const uint32_t blocks = a.blocks_q + a.blocks_k;
     if (blocks == 0) return SLIKL_OK;
     const auto kernel = pick(*p, Forward{});
@@ -1035,7 +1037,7 @@ slikl_status run_gradient(const slikl_qk_problem *p, const slikl_qk_tensors *t, 
                           int sms, cudaStream_t st) {
     Args a = make_args(p, t);
     a.partial = partial;
-    share_blocks(a, p->D, sms, kGradPerSm);
+    share_blocks(a, p->D, sms, kGradPerSm, 1.5);
     if (a.blocks_q + a.blocks_k > 0) {
         const auto kernel = pick(*p, Gradient{});
         kernel<<<a.blocks_q + a.blocks_k, kThreads, 0, st>>>(a);
