@@ -64,6 +64,11 @@ __device__ __forceinline__ uint32_t order_of(float x) {
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
+// The score that an order number stands for, where it is one: not for NaN and zero, which have several.
+__device__ __forceinline__ float score_of(uint32_t o) {
+    return __uint_as_float(o & 0x80000000u ? o & 0x7fffffffu : ~o);
+}
+
 // Exclusive prefix of v over the block.
 __device__ int block_prefix(int v, int *warp_sums) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -208,7 +213,6 @@ __global__ void __launch_bounds__(kChoose) __cluster_dims__(CS, 1, 1) evict_choo
     for (uint32_t j0 = 0; j0 < slice1 - slice0; j0 += TILE) {
         if (!once) read_tile(first + j0);
         uint32_t is_sure = 0, is_tied = 0;       // bit k: this lane's row of round k
-        int n_sure = 0, n_tied = 0;
 #pragma unroll
         for (int k = 0; k < ROUNDS; ++k) {
             const bool d = decided >> k & 1;
@@ -217,24 +221,19 @@ __global__ void __launch_bounds__(kChoose) __cluster_dims__(CS, 1, 1) evict_choo
             const bool t = d && wanted > 0 && order[k] == prefix;
             is_sure |= (uint32_t)s << k;
             is_tied |= (uint32_t)t << k;
-            n_sure += __popc(__ballot_sync(0xffffffffu, s));
-            n_tied += __popc(__ballot_sync(0xffffffffu, t));
         }
+        const int n_sure = __reduce_add_sync(0xffffffffu, __popc(is_sure));
+        const int n_tied = __reduce_add_sync(0xffffffffu, __popc(is_tied));
         __syncthreads();
         if (lane == 0) more[0][warp] = n_sure, more[1][warp] = n_tied;
         __syncthreads();
-        int w_sure = lane < warp ? more[0][lane] : 0, w_tied = lane < warp ? more[1][lane] : 0;
-        int t_sure = more[0][lane], t_tied = more[1][lane];
+        const int c_sure = more[0][lane], c_tied = more[1][lane];
+        int g = sure + __reduce_add_sync(0xffffffffu, lane < warp ? c_sure : 0);
+        int e = tied + __reduce_add_sync(0xffffffffu, lane < warp ? c_tied : 0);
+        sure += __reduce_add_sync(0xffffffffu, c_sure);
+        tied += __reduce_add_sync(0xffffffffu, c_tied);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            w_sure += __shfl_xor_sync(0xffffffffu, w_sure, o);
-            w_tied += __shfl_xor_sync(0xffffffffu, w_tied, o);
-            t_sure += __shfl_xor_sync(0xffffffffu, t_sure, o);
-            t_tied += __shfl_xor_sync(0xffffffffu, t_tied, o);
-        }
-        int g = sure + w_sure, e = tied + w_tied;
-        // (no loop for warps that keep nothing)
-        for (int k = 0; k < (n_sure + n_tied ? ROUNDS : 0); ++k) {
+        for (int k = 0; k < ROUNDS; ++k) {
             const bool s = is_sure >> k & 1, t = is_tied >> k & 1;
             const uint32_t bs = __ballot_sync(0xffffffffu, s), bt = __ballot_sync(0xffffffffu, t);
             const uint32_t below = (1u << lane) - 1;
@@ -243,13 +242,14 @@ __global__ void __launch_bounds__(kChoose) __cluster_dims__(CS, 1, 1) evict_choo
                 const int place = g + __popc(bs & below) + min(before, left);
                 const uint32_t j = first + j0 + 32 * k;
                 kept[place] = (int32_t)j;
-                if (out) out[place] = scores[j];
+                if (out) {
+                    const float x = score_of(order[k]);
+                    out[place] = x == 0.f || x != x ? scores[j] : x;
+                }
             }
             g += __popc(bs);
             e += __popc(bt);
         }
-        sure += t_sure;
-        tied += t_tied;
     }
     for (uint32_t j = stay + rank * kChoose + threadIdx.x; j < budget; j += CS * kChoose) {
         kept[j] = -1;
