@@ -2,11 +2,12 @@
 // include/slikl.h).
 //
 // evict_choose finds, for each sequence, the score of the last row that stays by a radix select
-// over order-preserving integers (three passes of 11, 11 and 10 bits), then walks the rows in
+// over order-preserving integers (four passes of 8 bits), then walks the rows in
 // order and writes the kept ones behind one another. It is bound by latency: a pass over the scores,
 // which L2 holds, and the barriers between. So a long sequence is shared by a cluster of eight blocks,
 // whose histograms and counts the others read from its shared memory (one block took 127 us for
-// sequences of up to 131072 rows). evict_copy moves the caches' rows, bound by HBM.
+// sequences of up to 131072 rows; with three passes of 11 bits each block's reads of the others' 2048
+// bins, and their prefix sums, took two thirds of a pass). evict_copy moves the caches' rows, bound by HBM.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -17,7 +18,7 @@ namespace slikl {
 namespace {
 
 constexpr int kChoose = 1024;         // threads of evict_choose
-constexpr int kBins = 2048;
+constexpr int kBins = 256;
 
 struct EvictArgs {
     int layout_k, n_caches;
@@ -69,31 +70,6 @@ __device__ __forceinline__ float score_of(uint32_t o) {
     return __uint_as_float(o & 0x80000000u ? o & 0x7fffffffu : ~o);
 }
 
-// Exclusive prefix of v over the block.
-__device__ int block_prefix(int v, int *warp_sums) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int x = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-    }
-    if (lane == 31) warp_sums[warp] = x;
-    __syncthreads();
-    if (warp == 0) {
-        const int own = warp_sums[lane];
-        int w = own;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, w, o);
-            if (lane >= o) w += y;
-        }
-        warp_sums[lane] = w - own;
-    }
-    __syncthreads();
-    return x - v + warp_sums[warp];
-}
-
 // CS blocks share a sequence; a tile of a block's slice is ROUNDS rows for each of its threads, which hold
 // their order numbers in registers: row 32 k of a warp's share (32 ROUNDS neighbours) and the lane's place.
 // The usual slice is one tile, read once; a longer one is read again for every pass.
@@ -102,9 +78,9 @@ __global__ void __launch_bounds__(kChoose) __cluster_dims__(CS, 1, 1) evict_choo
     namespace cg = cooperative_groups;
     constexpr bool SMALL = CS == 1 && ROUNDS == 1;
     constexpr uint32_t SHARE = 32 * ROUNDS, TILE = kChoose * ROUNDS;
-    __shared__ int bins[SMALL ? 1 : 3][SMALL ? 1 : kBins];   // of each pass: the other blocks may still
+    __shared__ int bins[SMALL ? 1 : 4][SMALL ? 1 : kBins];   // of each pass: the other blocks may still
                                                              // read an earlier one
-    __shared__ int warp_sums[32], more[2][32];
+    __shared__ int more[2][32];
     __shared__ uint32_t found_bin;
     __shared__ int found_above, counts[2];
     let_next_start();                    // evict_copy
@@ -149,43 +125,51 @@ __global__ void __launch_bounds__(kChoose) __cluster_dims__(CS, 1, 1) evict_choo
         left -= __syncthreads_count(decided && order[0] > prefix);
     } else if (wanted > 0 && !SMALL) {
         uint32_t mask = 0;
-        for (int i = threadIdx.x; i < 3 * kBins; i += kChoose) bins[0][i] = 0;
+        for (int i = threadIdx.x; i < 4 * kBins; i += kChoose) bins[0][i] = 0;
         __syncthreads();
-        for (int pass = 0; pass < 3; ++pass) {
-            const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, width = pass == 2 ? 10 : 11;
+        for (int pass = 0; pass < 4; ++pass) {
+            const int shift = 24 - 8 * pass;
             for (uint32_t j = 0; j < slice1 - slice0; j += TILE) {
                 if (!once) read_tile(first + j);
 #pragma unroll
                 for (int k = 0; k < ROUNDS; ++k)
                     if ((decided >> k & 1) && (order[k] & mask) == prefix)
-                        atomicAdd(&bins[pass][(order[k] >> shift) & ((1u << width) - 1)], 1);
+                        atomicAdd(&bins[pass][order[k] >> shift & 255], 1);
             }
             if (CS == 1) __syncthreads();
             else cluster.sync();
-            // thread i holds bins 2047 - 2i and 2046 - 2i: the prefix runs from the highest bin
-            const int bin = kBins - 2 - 2 * threadIdx.x;
-            const int m1 = bins[pass][bin], m0 = bins[pass][bin + 1];
-            int h1 = 0, h0 = 0;
-            if (CS == 1) {
-                h1 = m1, h0 = m0;
-            } else {
+            // thread i < 256 holds bin 255 - i: the prefix runs from the highest bin
+            const int bin = kBins - 1 - (int)threadIdx.x;
+            int h = 0, mine = 0, x = 0;
+            if (threadIdx.x < kBins) {
+                mine = bins[pass][bin];
+                if (CS == 1) {
+                    h = mine;
+                } else {
 #pragma unroll
-                for (int r = 0; r < CS; ++r) {
-                    const int2 h = *reinterpret_cast<const int2 *>(cluster.map_shared_rank(&bins[pass][bin], r));
-                    h1 += h.x, h0 += h.y;
+                    for (int r = 0; r < CS; ++r) h += *cluster.map_shared_rank(&bins[pass][bin], r);
                 }
-            }
-            const int above = block_prefix(h0 + h1, warp_sums);
-            if (above < left && left <= above + h0 + h1) {
-                const bool upper = left <= above + h0;
-                found_bin = bin + (upper ? 1 : 0);
-                found_above = above + (upper ? 0 : h0);
+                x = h;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, x, o);
+                    if (lane >= o) x += y;
+                }
+                if (lane == 31) more[0][warp] = x;
             }
             __syncthreads();
-            const int found = found_bin;
-            above_mine += (bin > found ? m1 : 0) + (bin + 1 > found ? m0 : 0);
-            prefix |= (uint32_t)found << shift;
-            mask |= ((1u << width) - 1) << shift;
+            if (threadIdx.x < kBins) {
+                int above = x - h;
+                for (int w = 0; w < warp; ++w) above += more[0][w];
+                if (above < left && left <= above + h) {
+                    found_bin = bin;
+                    found_above = above;
+                }
+            }
+            __syncthreads();
+            if (threadIdx.x < kBins && bin > (int)found_bin) above_mine += mine;
+            prefix |= found_bin << shift;
+            mask |= 255u << shift;
             left -= found_above;
         }
     }
@@ -193,12 +177,16 @@ __global__ void __launch_bounds__(kChoose) __cluster_dims__(CS, 1, 1) evict_choo
     // places (counts[1])
     int sure = 0, tied = 0;
     if (CS > 1) {
-        const int total = block_prefix(above_mine, warp_sums) + above_mine;
-        if (threadIdx.x == kChoose - 1) {
+        // (above_mine: of the first 256 threads, eight warps)
+        const int sum = __reduce_add_sync(0xffffffffu, above_mine);
+        if (lane == 0) more[1][warp] = sum;
+        __syncthreads();
+        if (threadIdx.x == 0) {
             const uint32_t from = max(lo, slice0), to = min(hi, slice1);
-            const uint32_t inside = from < to ? to - from : 0;
-            counts[0] = total + (int)(slice1 - slice0 - inside);
-            counts[1] = wanted > 0 ? bins[SMALL ? 0 : 2][SMALL ? 0 : prefix & 1023] : 0;
+            int total = (int)(slice1 - slice0 - (from < to ? to - from : 0));
+            for (int w = 0; w < kBins / 32; ++w) total += more[1][w];
+            counts[0] = total;
+            counts[1] = wanted > 0 ? bins[SMALL ? 0 : 3][SMALL ? 0 : prefix & 255] : 0;
         }
         cluster.sync();
         for (int r = 0; r < (int)rank; ++r) {

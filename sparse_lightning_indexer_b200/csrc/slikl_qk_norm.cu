@@ -990,7 +990,8 @@ void share_blocks(Args &a, int64_t D, int sms, int per_sm, double few) {
     }
     if ((uint64_t)blocks[0] + blocks[1] > most) {
         const uint32_t share = (uint32_t)(most * (cost[1] / (cost[0] + cost[1])) + 0.5);
-        blocks[1] = blocks[1] == 0 ? 0 : std::min(blocks[1], std::max(share, 1u));
+        const uint32_t least_q = blocks[0] ? 1 : 0, least_k = blocks[1] ? 1 : 0;
+        blocks[1] = std::min(blocks[1], std::min(std::max(share, least_k), most - least_q));
         blocks[0] = std::min(blocks[0], most - blocks[1]);
     }
     for (int i = 0; i < 2; ++i)

@@ -109,6 +109,43 @@ def test_forward_and_gradient(case, source):
             check_checkpoint(fwd["checkpoint_" + n], s["x"], pos[n])
 
 
+@pytest.mark.parametrize("T1,N1,T2", [(6, 1, 24717), (4, 5, 63928), (40000, 1, 3), (700, 64, 1), (0, 4, 30000)])
+@pytest.mark.parametrize("source", ["x", "x8"])
+def test_sides_of_very_different_sizes(T1, N1, T2, source):
+    """A side of a few rows beside one of many gets its rows done, with the same bits as alone."""
+    D, R = 64, 32
+    q, k = make(21, T1, N1, D, R, BF, "layer"), make(22, T2, 1, D, R, BF, "rms")
+    cs = dev(table(300, R))
+    pos = {n: dev(torch.arange(t, dtype=torch.int32) % 300) for n, t in (("q", T1), ("k", T2))}
+    xq, xk = dev(q["x"]), dev(k["x"])
+    if source == "x8":
+        xq, xk = sli.checkpoint_pack(xq), sli.checkpoint_pack(xk)
+    kw = dict(norm_q="layer", norm_k="rms", layout_q="TND", layout_k="TND")
+    keep = source == "x"
+
+    def fill(*shape):
+        return torch.full(shape, float("nan"), dtype=BF, device="cuda")
+
+    both = sli.qk_norm_rope(xq, xk, cs, pos_q=pos["q"], pos_k=pos["k"], checkpoint=keep,
+                            out=dict(q=fill(T1, N1, D), k=fill(T2, 1, D)), **kw)
+    one = sli.qk_norm_rope(xq, None, cs, pos_q=pos["q"], checkpoint=keep, **kw)
+    two = sli.qk_norm_rope(None, xk, cs, pos_k=pos["k"], checkpoint=keep, **kw)
+    assert torch.equal(both["q"], one["q"]) and torch.equal(both["k"], two["k"])
+    if keep:
+        for n, alone in (("q", one), ("k", two)):
+            c, d = both["checkpoint_" + n], alone["checkpoint_" + n]
+            assert torch.equal(c.values.view(torch.uint8), d.values.view(torch.uint8)) and torch.equal(c.scale, d.scale)
+    dq, dk = dev(q["dy"]), dev(k["dy"])
+    both = sli.qk_norm_rope_grad(dq, dk, xq, xk, cs, pos_q=pos["q"], pos_k=pos["k"],
+                                 out=dict(dx_q=fill(T1, N1, D), dx_k=fill(T2, 1, D)), **kw)
+    at = {n: dequant(x) if source == "x8" else s["x"].double() for n, x, s in (("q", xq, q), ("k", xk, k))}
+    for n, s, kind in (("q", q, "layer"), ("k", k, "rms")):
+        want = ref.norm_rope_grad(s["dy"].double(), at[n], kind, None, cs.cpu(), pos[n].cpu(), R, False, EPS, BF)
+        for what in ("dx", "dgain", "dbias"):
+            if want[what] is not None and both[f"{what}_{n}"].numel():
+                inside(f"{what}_{n}", both[f"{what}_{n}"], want[what])
+
+
 def check_checkpoint(c, x, pos=None):
     live = (pos >= 0)[:, None] if pos is not None else torch.ones(x.shape[:-1], dtype=torch.bool)
     x = torch.where(live[..., None], x.double(), 0.0)
