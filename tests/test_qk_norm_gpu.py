@@ -472,3 +472,38 @@ def test_projected_gradient(layout, source, mode):
     qk["pos_k"][0] = 400
     res = sli.grad_projected(xq, xk, dev(wl.w), dev(wl.p), dev(wl.idx), dev(cs), **qk, **idx)
     assert sli.slikl_read_device_status(res["workspace"].data_ptr()) == sli.SLIKL_DEV_BAD_POSITION
+
+
+@pytest.mark.parametrize("T1,T2", [(0, 40), (30, 0)])
+def test_projected_gradient_without_queries_or_keys(T1, T2):
+    """Empty TND sides: what is there gets zero gradients."""
+    N1, D, K = 8, 64, 16
+    q, k = make(91, T1, N1, D, 32, BF, "rms"), make(92, T2, 1, D, 32, BF, "layer")
+    cu = [torch.tensor([0, t], dtype=torch.int32, device="cuda") for t in (T1, T2)]
+    pos = [torch.arange(t, dtype=torch.int32, device="cuda") for t in (T1, T2)]
+    r = sli.grad_projected(dev(q["x"]), dev(k["x"]), torch.rand(T1, N1, device="cuda"),
+                           torch.rand(T1, 1, K, device="cuda"),
+                           torch.full((T1, 1, K), -1, dtype=torch.int32, device="cuda"), dev(table(50, 32)),
+                           pos_q=pos[0], pos_k=pos[1], norm_k="layer", layout_q="TND", layout_k="TND",
+                           cu_seqlens_q=cu[0], cu_seqlens_k=cu[1])
+    torch.cuda.synchronize()
+    assert sli.slikl_read_device_status(r["workspace"].data_ptr()) == 0
+    for n in ("dx_q", "dx_k", "dgain_q", "dgain_k", "dbias_k"):
+        assert (r[n] == 0).all(), n
+
+
+def test_two_streams_at_once():
+    """Calls in flight on two streams do not disturb each other."""
+    cs = dev(table(2000, 64))
+    sides = [(make(31 + i, 2000, 16, 128, 64, BF, "layer"), make(33 + i, 2000, 1, 128, 64, BF, "rms")) for i in range(2)]
+    pos = torch.arange(2000, dtype=torch.int32, device="cuda")
+    kw = dict(pos_q=pos, pos_k=pos, norm_q="layer", layout_q="TND", layout_k="TND")
+    args = [tuple(dev(s[n]) for n in ("dy", "x") for s in two) for two in sides]
+    want = [sli.qk_norm_rope_grad(*a, cs, **kw) for a in args]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[sli.qk_norm_rope_grad(*a, cs, stream=s, **kw) for s, a in zip(streams, args)] for _ in range(20)]
+    torch.cuda.synchronize()
+    for turn in got:
+        for w, g in zip(want, turn):
+            assert all(torch.equal(w[n], g[n]) for n in w if n != "workspace" and w[n] is not None)
