@@ -449,8 +449,8 @@ SLIKL_API slikl_status slikl_grad_recompute_p(const slikl_problem *problem,
  * 8-bit checkpoints. A checkpoint of x is, for each head of each row, scale = max|x| / 448 (fp32;
  * 0 for a zero row, at least the smallest normal fp32 number otherwise) and the D values x / scale
  * rounded to e4m3. The forward call can write one beside y in the same pass, both calls can read
- * one in place of x, and the gradient is then the one at scale * value. A value that is not
- * finite makes its whole row of the checkpoint NaN, scale excepted.
+ * one in place of x, and the gradient is then the one at scale * value. A NaN stays
+ * one; an infinity makes its row's scale infinite, and the whole row reads back as NaN.
  *
  * Positions: row t stands at positions[t], or, where positions is NULL, at t % S. A row at -1 is
  * padding: its y, checkpoint and dx are 0 and it takes no part in dgain and dbias. Any other
@@ -577,7 +577,7 @@ SLIKL_API slikl_status slikl_grad_projected(const slikl_problem *problem,
  */
 typedef struct {
     const int32_t *sparse_indices;  /* int32 [.., 1, topk] as in slikl_tensors                   */
-    const float *weights;           /* fp32  [.., 1, topk]; not read at invalid slots' values    */
+    const float *weights;           /* fp32  [.., 1, topk]; at invalid slots it may hold anything */
     const int32_t *cu_seqlens_q;    /* int32 [B+1], TND query side only, else NULL               */
     const int32_t *cu_seqlens_k;    /* int32 [B+1], TND key side only, else NULL                 */
     const float *scores;            /* fp32  [B,S2] / [T2], or NULL: zeros                       */

@@ -7,7 +7,7 @@
 // which L2 holds, and the barriers between. So a long sequence is shared by a cluster of eight blocks,
 // whose histograms and counts the others read from its shared memory (one block took 127 us for
 // sequences of up to 131072 rows; with three passes of 11 bits each block's reads of the others' 2048
-// bins, and their prefix sums, took two thirds of a pass). evict_copy moves the caches' rows, bound by HBM.
+// bins, and their prefix sums, took two thirds of a pass; 21 us now). evict_copy moves the caches' rows, bound by HBM.
 #include <cooperative_groups.h>
 
 #include <algorithm>

@@ -6,15 +6,20 @@
 // bounding the call instead is the scattered additions. 64-bit additions to global memory, one a
 // slot, run at 128 G/s on B200 however far apart the keys are (147 us for 16.8 M slots over 131072
 // keys, seven times the floor) and slower on few keys. So sums are kept in shared memory, as 32-bit
-// additions that return what was there: a carry out of the low word, and the high word of a large
-// weight, are rare and go their own way. All rows of a batch name the same keys, so a block reads a
+// additions that return what was there; a carry out of the low word and the high word of a large weight
+// go their own way. All rows of a batch name the same keys, so a block reads a
 // stretch of the batch's slots without looking where rows begin. Two forms:
 //   weights_direct  few slots a batch (a decoding step): a block owns a chunk of a batch's keys, reads
 //                   all of the batch's slots, keeps both words and writes the chunk's result: one
 //                   launch and no workspace;
-//   weights_split   else: blocks share a batch's slots, keep the low words of up to 45056 keys (larger
+//   weights_split   else: blocks share a batch's slots, keep the low words of up to 55296 keys (larger
 //                   ranges are covered by several blocks that read the same slots, from L2 mostly)
 //                   and add them to 64-bit sums in the workspace once; weights_finish makes the result.
+// Measured on B200: 4 us for 32 rows of 2048 slots over 8192 keys each, 19 us for 8.4 M slots over 4096 keys
+// (3.5 TB/s of slots; floor 10.4), 68 us for 16.8 M over 131072 (floor 21; three blocks read each slot). The
+// split form is bound by its instructions (issue slots 58 %, the integer pipe 56 % in use) and by the
+// latency of its loads between them; more loads on their way, by registers or through shared memory,
+// were no faster.
 #include <algorithm>
 
 #include "slikl_common.cuh"
@@ -227,10 +232,8 @@ __global__ void __launch_bounds__(kSplitThreads) weights_split(WeightArgs a, int
     let_next_start();         // weights_finish
     const Batch r = batch_of(a, a.first_batch + blockIdx.z);
     const int64_t slots = r.end - r.begin;
-    // (shares of whole fours, so that they are aligned alike)
-    const int64_t begin = r.begin + ((slots * blockIdx.y / gridDim.y) & ~(int64_t)3);
-    const int64_t end = blockIdx.y + 1 == gridDim.y ? r.end
-                                                    : r.begin + ((slots * (blockIdx.y + 1) / gridDim.y) & ~(int64_t)3);
+    const int64_t begin = r.begin + slots * blockIdx.y / gridDim.y;
+    const int64_t end = r.begin + slots * (blockIdx.y + 1) / gridDim.y;
     if (begin == end) return;
     for (int64_t first = (int64_t)blockIdx.x * chunk; first < r.used;
          first += (int64_t)gridDim.x * chunk) {

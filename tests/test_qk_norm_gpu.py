@@ -310,6 +310,38 @@ def test_zero_rows_have_finite_results():
         assert (r["q"] == 0).all() and torch.isfinite(b["dx_q"]).all() and (b["dgain_q"] == 0).all()
 
 
+def test_smallest_eps():
+    """Rows of zeros and padding rows with r up to 1e19, whose cube is beyond fp32."""
+    s = make(21, 12, 8, 128, 64, BF, "rms")
+    x, cs = s["x"].clone(), table(12, 64)
+    x[3] = 0
+    pos = torch.arange(12, dtype=torch.int32)
+    pos[7] = -1
+    for kind in ("rms", "layer"):
+        kw = dict(pos_q=dev(pos), layout_q="TND", norm_q=kind, gain_q=dev(s["gain"]), eps=1e-38)
+        b = sli.qk_norm_rope_grad(dev(s["dy"]), None, dev(x), None, dev(cs), **kw)
+        want = ref.norm_rope_grad(s["dy"].double(), x.double(), kind, s["gain"], cs, pos, 64, False, 1e-38, BF)
+        inside("dx", b["dx_q"], want["dx"])
+        inside("dgain", b["dgain_q"], want["dgain"])
+        assert (b["dx_q"][7] == 0).all()
+
+
+@pytest.mark.parametrize("pairs", [False, True])
+@pytest.mark.parametrize("N", [1, 16])
+def test_dims_behind_the_rotated_ones_do_not_meet(pairs, N):
+    """Without a norm an infinity or NaN in a dim that is not turned stays there."""
+    s = make(22, 4000, N, 128, 64, FP, "none")
+    x, cs = s["x"].clone(), table(50, 64)
+    x[5, 0, 70], x[9, N - 1, 127], x[3990, 0, 64] = float("inf"), float("nan"), float("-inf")
+    kw = dict(pos_q=dev(torch.arange(4000, dtype=torch.int32) % 50), layout_q="TND", norm_q="none",
+              rot_layout="pairs" if pairs else "halves")
+    y = sli.qk_norm_rope(dev(x), None, dev(cs), **kw)["q"].cpu()
+    dx = sli.qk_norm_rope_grad(dev(x), None, dev(x), None, dev(cs), **kw)["dx_q"].cpu()
+    for got in (y, dx):
+        assert torch.equal(torch.isfinite(got), torch.isfinite(x))
+        assert torch.equal(got[..., 64:][torch.isfinite(x[..., 64:])], x[..., 64:][torch.isfinite(x[..., 64:])])
+
+
 def test_in_place():
     s = make(15, 100, 16, 128, 64, BF, "rms")
     cs = table(100, 64)
