@@ -76,7 +76,7 @@ def build_torch(force: bool = False) -> str:
     """Compile csrc/slikl_torch.cpp against torch's headers and libslikl.so; returns its path."""
     src = os.path.join(CSRC, "slikl_torch.cpp")
     headers = glob.glob(os.path.join(INCLUDE, "*.h"))
-    if not force and not _stale(TORCH_LIB, [src] + headers):
+    if not force and not _stale(TORCH_LIB, [src, os.path.abspath(__file__)] + headers):
         return TORCH_LIB
     import sysconfig
 
@@ -86,11 +86,14 @@ def build_torch(force: bool = False) -> str:
                 sysconfig.get_paths()["include"],
                 os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")]
     tmp = TORCH_LIB + f".tmp{os.getpid()}"
-    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+    # g++, which nvcc takes for its host code too, whatever $CXX says; and the C++ library that torch
+    # has loaded: one linked in statically, where the compiler finds no other, is a second one in the
+    # process, and its streams crash
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            *[a for i in includes for a in ("-isystem", i)], "-I", INCLUDE, src, "-o", tmp,
            "-L", PKG, "-lslikl", "-L", os.path.join(troot, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
-           "-ltorch", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
+           "-ltorch", "-ltorch_python", "-l:libstdc++.so.6", "-Wl,-rpath,$ORIGIN"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         sys.stderr.write(res.stdout + res.stderr)
