@@ -11,7 +11,6 @@ sm_100 device is present the calls raise.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 from typing import NamedTuple, Optional, Sequence
 
@@ -739,18 +738,6 @@ def _load_binding():
     return _binding
 
 
-def _on_stream(f):
-    """f with its `stream` argument, where one is given, as the current stream: what f allocates
-    then belongs to that stream too."""
-    @functools.wraps(f)
-    def call(*args, stream=None, **kw):
-        if stream is None:
-            return f(*args, **kw)
-        with torch.cuda.stream(stream):
-            return f(*args, **kw)
-    return call
-
-
 def _sources(x_q, x_k):
     """(tensor, scale) of x_q and of x_k, or of their Checkpoints, and the type those stand for."""
     vq, sq, tq = x_q if type(x_q) is Checkpoint else (x_q, None, None)
@@ -760,11 +747,10 @@ def _sources(x_q, x_k):
     return vq, sq, vk, sk, tq or tk
 
 
-@_on_stream
 def qk_norm_rope(x_q, x_k, cos_sin=None, *, pos_q=None, pos_k=None, gain_q=None, gain_k=None,
                  bias_q=None, bias_k=None, norm_q="rms", norm_k="rms", rot_layout="halves",
                  eps=1e-6, layout_q="BSND", layout_k="BSND", checkpoint=False, out=None,
-                 status=None):
+                 status=None, stream=None):
     """q and k of the indexer from the outputs of their projections (slikl_qk_norm_rope).
 
     x_q [B,S1,N1,D] / [T1,N1,D], x_k [B,S2,N2,D] / [T2,N2,D] in float16 or bfloat16, or a
@@ -780,7 +766,8 @@ def qk_norm_rope(x_q, x_k, cos_sin=None, *, pos_q=None, pos_k=None, gain_q=None,
     rc, q, k, *kept = _load_binding().qk_forward(
         *_sources(x_q, x_k), cos_sin, pos_q, pos_k, gain_q, gain_k, bias_q, bias_k,
         _NORMS.get(norm_q, -1), _NORMS.get(norm_k, -1), _ROTS.get(rot_layout, -1), eps,
-        _LAYOUTS.get(layout_q, -1), _LAYOUTS.get(layout_k, -1), True, checkpoint, out_q, out_k, status)
+        _LAYOUTS.get(layout_q, -1), _LAYOUTS.get(layout_k, -1), True, checkpoint, out_q, out_k, status,
+        stream)
     if rc != SLIKL_OK:
         raise SliklError(rc, "slikl_qk_norm_rope")
     res = dict(q=q, k=k)
@@ -790,10 +777,10 @@ def qk_norm_rope(x_q, x_k, cos_sin=None, *, pos_q=None, pos_k=None, gain_q=None,
     return res
 
 
-@_on_stream
 def qk_norm_rope_grad(dq, dk, x_q, x_k, cos_sin=None, *, pos_q=None, pos_k=None, gain_q=None,
                       gain_k=None, norm_q="rms", norm_k="rms", rot_layout="halves", eps=1e-6,
-                      layout_q="BSND", layout_k="BSND", out=None, workspace=None, status=None):
+                      layout_q="BSND", layout_k="BSND", out=None, workspace=None, status=None,
+                      stream=None):
     """The gradient of qk_norm_rope at x (or its Checkpoint): dq, dk as grad() returns them back to
     the projections. Returns dict(dx_q, dx_k, dgain_q, dgain_k, dbias_q, dbias_k, workspace); a
     side without a norm has no dgain, one without a layer norm no dbias. `out` may supply
@@ -802,28 +789,27 @@ def qk_norm_rope_grad(dq, dk, x_q, x_k, cos_sin=None, *, pos_q=None, pos_k=None,
     rc, dx_q, dx_k, dgain_q, dbias_q, dgain_k, dbias_k, ws = _load_binding().qk_gradient(
         dq, dk, *_sources(x_q, x_k), cos_sin, pos_q, pos_k, gain_q, gain_k,
         _NORMS.get(norm_q, -1), _NORMS.get(norm_k, -1), _ROTS.get(rot_layout, -1), eps,
-        _LAYOUTS.get(layout_q, -1), _LAYOUTS.get(layout_k, -1), out_q, out_k, workspace, status)
+        _LAYOUTS.get(layout_q, -1), _LAYOUTS.get(layout_k, -1), out_q, out_k, workspace, status, stream)
     if rc != SLIKL_OK:
         raise SliklError(rc, "slikl_qk_norm_rope_grad")
     return dict(dx_q=dx_q, dx_k=dx_k, dgain_q=dgain_q, dgain_k=dgain_k, dbias_q=dbias_q,
                 dbias_k=dbias_k, workspace=ws)
 
 
-@_on_stream
-def checkpoint_pack(x) -> Checkpoint:
+def checkpoint_pack(x, *, stream=None) -> Checkpoint:
     """8-bit checkpoint of x [.., N, D] (float16 or bfloat16, contiguous, D 64 or 128): one e4m3
     value an element and one fp32 scale, max|x| / 448, for each of the D-long rows."""
     rows = _rows(x)
     rc, _, _, values, scale, _, _ = _load_binding().qk_forward(
         rows, None, None, None, None, None, None, None, None, None, None, None, SLIKL_NORM_NONE,
-        SLIKL_NORM_NONE, SLIKL_ROT_HALVES, 1.0, SLIKL_TND, SLIKL_TND, False, True, None, None, None)
+        SLIKL_NORM_NONE, SLIKL_ROT_HALVES, 1.0, SLIKL_TND, SLIKL_TND, False, True, None, None, None,
+        stream)
     if rc != SLIKL_OK:
         raise SliklError(rc, "slikl_qk_norm_rope")
     return Checkpoint(values.view(x.shape), scale.view(x.shape[:-1]), x.dtype)
 
 
-@_on_stream
-def checkpoint_unpack(c: Checkpoint) -> torch.Tensor:
+def checkpoint_unpack(c: Checkpoint, *, stream=None) -> torch.Tensor:
     """The tensor that a checkpoint stands for, scale * values rounded to its 16-bit type."""
     rows = _rows(c.values)
     if c.scale.shape != c.values.shape[:-1] or not c.scale.is_contiguous():
@@ -831,7 +817,7 @@ def checkpoint_unpack(c: Checkpoint) -> torch.Tensor:
     rc, x, *_ = _load_binding().qk_forward(
         rows, c.scale.view(rows.shape[:-1]), None, None, c.dtype, None, None, None, None, None, None,
         None, SLIKL_NORM_NONE, SLIKL_NORM_NONE, SLIKL_ROT_HALVES, 1.0, SLIKL_TND, SLIKL_TND, True,
-        False, None, None, None)
+        False, None, None, None, stream)
     if rc != SLIKL_OK:
         raise SliklError(rc, "slikl_qk_norm_rope")
     return x.view(c.values.shape)
@@ -844,13 +830,12 @@ def _rows(t):
     return t.view(-1, 1, t.shape[-1]) if t.numel() else t.new_empty(0, 1, t.shape[-1])
 
 
-@_on_stream
 def grad_projected(x_q, x_k, w, attn_softmax_l1norm, sparse_indices, cos_sin=None, *, pos_q=None,
                    pos_k=None, gain_q=None, gain_k=None, bias_q=None, bias_k=None, norm_q="rms",
                    norm_k="rms", rot_layout="halves", eps=1e-6, layout_q="BSND", layout_k="BSND",
                    cu_seqlens_q=None, cu_seqlens_k=None, deterministic=False, out=None,
                    workspace=None, dk_path="auto", key_range_bound=0, loss=False, seq_used_q=None,
-                   seq_used_k=None):
+                   seq_used_k=None, stream=None):
     """grad() from the outputs of the projections, or from their checkpoints: q and k as
     qk_norm_rope forms them, the indexer's gradient, and dq, dk back as qk_norm_rope_grad takes
     them, in one call (slikl_grad_projected). Returns dict(dx_q, dx_k, dgain_*, dbias_*, dw,
@@ -863,7 +848,7 @@ def grad_projected(x_q, x_k, w, attn_softmax_l1norm, sparse_indices, cos_sin=Non
         gain_k, bias_q, bias_k, _NORMS.get(norm_q, -1), _NORMS.get(norm_k, -1), _ROTS.get(rot_layout, -1),
         eps, _LAYOUTS.get(layout_q, -1), _LAYOUTS.get(layout_k, -1), cu_seqlens_q, cu_seqlens_k,
         deterministic, _DK_PATHS[dk_path], key_range_bound, loss, seq_used_q, seq_used_k, out_q, out_k,
-        workspace)
+        workspace, stream)
     if rc != SLIKL_OK:
         raise SliklError(rc, "slikl_grad_projected")
     res = dict(dx_q=dx_q, dx_k=dx_k, dgain_q=dgain_q, dgain_k=dgain_k, dbias_q=dbias_q, dbias_k=dbias_k,
@@ -900,25 +885,23 @@ def slikl_evict(problem: slikl_evict_problem, tensors: slikl_evict_tensors,
         raise SliklError(rc, "slikl_evict")
 
 
-@_on_stream
 def key_weights(weights, sparse_indices, scores, *, decay=1.0, layout_q="BSND", layout_k="BSND",
                 cu_seqlens_q=None, cu_seqlens_k=None, seq_used_q=None, seq_used_k=None,
-                key_range_bound=0, out=None, workspace=None, status=None):
+                key_range_bound=0, out=None, workspace=None, status=None, stream=None):
     """decay * scores plus, for every key row, the weights of the slots that name it
     (slikl_key_weights): fp32 `weights` and int32 `sparse_indices` [B,S1,1,topk] / [T1,1,topk] (p of
     grad(), softmax_out, or p of grad_recompute_p), fp32 `scores` [B,S2] / [T2]. `out` may be
     `scores`. `status` (int32 [1]) receives the device flags. Returns dict(scores, workspace)."""
     rc, new, ws = _load_binding().key_weights(
         weights, sparse_indices, scores, decay, _LAYOUTS.get(layout_q, -1), _LAYOUTS.get(layout_k, -1),
-        cu_seqlens_q, cu_seqlens_k, seq_used_q, seq_used_k, key_range_bound, out, workspace, status)
+        cu_seqlens_q, cu_seqlens_k, seq_used_q, seq_used_k, key_range_bound, out, workspace, status, stream)
     if rc != SLIKL_OK:
         raise SliklError(rc, "slikl_key_weights")
     return dict(scores=new, workspace=ws)
 
 
-@_on_stream
 def evict(scores, caches: Sequence[torch.Tensor], budget, *, sinks=0, recent=0, layout_k="BSND",
-          cu_seqlens_k=None, seq_used_k=None, key_range_bound=0, out=None, status=None):
+          cu_seqlens_k=None, seq_used_k=None, key_range_bound=0, out=None, status=None, stream=None):
     """Cuts a cache to at most `budget` key rows a sequence (slikl_evict): the first `sinks`, the
     last `recent` and those with the highest fp32 `scores` [B,S2] / [T2]. `caches` are up to eight
     tensors [B,S2,..] / [T2,..] of any type whose rows (a multiple of 16 bytes) go along.
@@ -929,7 +912,8 @@ def evict(scores, caches: Sequence[torch.Tensor], budget, *, sinks=0, recent=0, 
     get = (out or {}).get
     rc, kept, lengths, new, outs = _load_binding().evict(
         scores, caches, budget, sinks, recent, _LAYOUTS.get(layout_k, -1), cu_seqlens_k, seq_used_k,
-        key_range_bound, get("kept"), get("lengths"), get("scores"), get("caches"), status)
+        key_range_bound, get("kept"), get("lengths"), get("scores"), get("caches"), status,
+        stream)
     if rc != SLIKL_OK:
         raise SliklError(rc, "slikl_evict")
     return dict(kept=kept, lengths=lengths, scores=new, caches=outs)

@@ -93,7 +93,7 @@ def build_torch(force: bool = False) -> str:
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            *[a for i in includes for a in ("-isystem", i)], "-I", INCLUDE, src, "-o", tmp,
            "-L", PKG, "-lslikl", "-L", os.path.join(troot, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
-           "-ltorch", "-ltorch_python", "-l:libstdc++.so.6", "-Wl,-rpath,$ORIGIN"]
+           "-ltorch_cuda", "-ltorch", "-ltorch_python", "-l:libstdc++.so.6", "-Wl,-rpath,$ORIGIN"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         sys.stderr.write(res.stdout + res.stderr)

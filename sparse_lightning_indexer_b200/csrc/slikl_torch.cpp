@@ -6,6 +6,7 @@
 //
 // Functions return (status code, outputs..); a refused argument raises ValueError.
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/utils/pybind.h>
@@ -18,6 +19,7 @@
 namespace py = pybind11;
 using at::Tensor;
 using Maybe = std::optional<Tensor>;
+using MaybeStream = std::optional<c10::Stream>;
 
 namespace {
 
@@ -44,8 +46,17 @@ P *address(const Tensor &t, const std::string &name, const at::Device &dev, at::
     return static_cast<P *>(t.data_ptr());
 }
 
+// (torch::empty and select go through the dispatcher, 1.2 us each time)
 Tensor fresh(at::IntArrayRef shape, at::ScalarType type, const at::Device &dev) {
-    return at::empty(shape, at::TensorOptions().dtype(type).device(dev));
+    return at::detail::empty_cuda(shape, type, dev, std::nullopt);
+}
+
+// A contiguous tensor of this shape in t's memory, `offset` elements in.
+Tensor part_of(const Tensor &t, int64_t offset, at::IntArrayRef shape) {
+    Tensor v = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(t.storage()), t.key_set(), t.dtype());
+    v.unsafeGetTensorImpl()->set_storage_offset(t.storage_offset() + offset);
+    v.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
+    return v;
 }
 
 // Elements from one row to the next of t [B, S, N, D] or [T, N, D] whose heads are dense.
@@ -153,16 +164,28 @@ Call enter(const SideArgs &q, const SideArgs &k, std::optional<at::ScalarType> t
     return c;
 }
 
+// For its life the tensors' device is the current one, and `stream`, where given, the current stream: what
+// is allocated then belongs to it too.
+struct On {
+    c10::cuda::OptionalCUDAStreamGuard stream;
+    c10::cuda::OptionalCUDAGuard device;
+    On(const at::Device &dev, const MaybeStream &s) {
+        if (s) stream.reset_stream(*s);
+        device.set_device(dev);
+    }
+};
+
 void *stream_of(const at::Device &dev) { return c10::cuda::getCurrentCUDAStream(dev.index()).stream(); }
 
 // Outputs q, k, and of each the checkpoint's values and scale where `keep`; `plain` = false: no q, k.
 py::tuple qk_forward(Maybe x_q, Maybe scale_q, Maybe x_k, Maybe scale_k, std::optional<at::ScalarType> type,
                      Maybe cos_sin, Maybe pos_q, Maybe pos_k, Maybe gain_q, Maybe gain_k, Maybe bias_q,
                      Maybe bias_k, int norm_q, int norm_k, int rot_layout, double eps, int layout_q,
-                     int layout_k, bool plain, bool keep, Maybe out_q, Maybe out_k, Maybe status) {
+                     int layout_k, bool plain, bool keep, Maybe out_q, Maybe out_k, Maybe status,
+                     MaybeStream stream) {
     Call c = enter({x_q, scale_q, pos_q, gain_q, bias_q, norm_q, layout_q},
                    {x_k, scale_k, pos_k, gain_k, bias_k, norm_k, layout_k}, type, cos_sin, rot_layout, eps, status);
-    const c10::cuda::OptionalCUDAGuard guard(c.dev);
+    const On on(c.dev, stream);
     Maybe y[2], kept[2], scale[2];
     for (int i = 0; i < 2; ++i) {
         if (!c.shape[i]) continue;
@@ -216,7 +239,7 @@ Grads enter_gradients(Call &c, const Maybe &out_q, const Maybe &out_k) {
         }
         t.dx = g.dx[i]->data_ptr();
         for (int which = 0; which < side.norm; ++which) {
-            g.sum[2 * i + which] = sums.select(0, row++);
+            g.sum[2 * i + which] = part_of(sums, c.pr.D * row++, {c.pr.D});
             float *p = g.sum[2 * i + which]->data_ptr<float>();
             if (which) t.dbias = p;
             else t.dgain = p;
@@ -238,10 +261,11 @@ size_t bytes_of(const Tensor &t) { return t.numel() * t.element_size(); }
 py::tuple qk_gradient(Maybe dq, Maybe dk, Maybe x_q, Maybe scale_q, Maybe x_k, Maybe scale_k,
                       std::optional<at::ScalarType> type, Maybe cos_sin, Maybe pos_q, Maybe pos_k, Maybe gain_q,
                       Maybe gain_k, int norm_q, int norm_k, int rot_layout, double eps, int layout_q,
-                      int layout_k, Maybe out_q, Maybe out_k, Maybe workspace, Maybe status) {
+                      int layout_k, Maybe out_q, Maybe out_k, Maybe workspace, Maybe status,
+                      MaybeStream stream) {
     Call c = enter({x_q, scale_q, pos_q, gain_q, {}, norm_q, layout_q}, {x_k, scale_k, pos_k, gain_k, {}, norm_k, layout_k},
                    type, cos_sin, rot_layout, eps, status);
-    const c10::cuda::OptionalCUDAGuard guard(c.dev);
+    const On on(c.dev, stream);
     for (int i = 0; i < 2; ++i) {
         if (!c.shape[i]) continue;
         const Maybe &dy = i ? dk : dq;
@@ -278,10 +302,10 @@ py::tuple grad_projected(Tensor x_q, Maybe scale_q, Tensor x_k, Maybe scale_k, s
                          Maybe gain_k, Maybe bias_q, Maybe bias_k, int norm_q, int norm_k, int rot_layout,
                          double eps, int layout_q, int layout_k, Maybe cu_q, Maybe cu_k, bool deterministic,
                          int dk_path, int64_t key_range_bound, bool loss, Maybe used_q, Maybe used_k, Maybe out_q,
-                         Maybe out_k, Maybe workspace) {
+                         Maybe out_k, Maybe workspace, MaybeStream stream) {
     Call c = enter({x_q, scale_q, pos_q, gain_q, bias_q, norm_q, layout_q},
                    {x_k, scale_k, pos_k, gain_k, bias_k, norm_k, layout_k}, type, cos_sin, rot_layout, eps, {});
-    const c10::cuda::OptionalCUDAGuard guard(c.dev);
+    const On on(c.dev, stream);
     const auto sq = *c.shape[0], sk = *c.shape[1];
     if (idx.dim() < 1) refuse("sparse_indices must be [.., 1, topk]");
     slikl_problem pr{};
@@ -330,14 +354,14 @@ py::tuple grad_projected(Tensor x_q, Maybe scale_q, Tensor x_k, Maybe scale_k, s
 
 py::tuple key_weights(Tensor weights, Tensor idx, Tensor scores, double decay, int layout_q, int layout_k,
                       Maybe cu_q, Maybe cu_k, Maybe used_q, Maybe used_k, int64_t key_range_bound, Maybe out,
-                      Maybe workspace, Maybe status) {
+                      Maybe workspace, Maybe status, MaybeStream stream) {
     const at::Device dev = scores.device();
     if (!dev.is_cuda() || layout_q < 0 || layout_k < 0) refuse("CUDA tensors and layouts BSND or TND are wanted");
     const auto shape = idx.sizes(), rows = scores.sizes();
     if (idx.dim() != (layout_q == SLIKL_BSND ? 4 : 3) || shape[shape.size() - 2] != 1 ||
         scores.dim() != (layout_k == SLIKL_BSND ? 2 : 1))
         refuse("sparse_indices must be [B,S1,1,topk] / [T1,1,topk], scores [B,S2] / [T2]");
-    const c10::cuda::OptionalCUDAGuard guard(dev);
+    const On on(dev, stream);
     slikl_problem pr{};
     pr.layout_q = layout_q;
     pr.layout_k = layout_k;
@@ -379,17 +403,18 @@ py::tuple key_weights(Tensor weights, Tensor idx, Tensor scores, double decay, i
 
 py::tuple evict(Tensor scores, std::vector<Tensor> caches, int64_t budget, int64_t sinks, int64_t recent,
                 int layout_k, Maybe cu_k, Maybe used_k, int64_t key_range_bound, Maybe out_kept, Maybe out_lengths,
-                Maybe out_scores, std::optional<std::vector<Tensor>> out_caches, Maybe status) {
+                Maybe out_scores, std::optional<std::vector<Tensor>> out_caches, Maybe status,
+                MaybeStream stream) {
     const at::Device dev = scores.device();
     if (!dev.is_cuda() || layout_k < 0) refuse("CUDA tensors and layout BSND or TND are wanted");
     const bool bsnd = layout_k == SLIKL_BSND;
     const auto rows = scores.sizes();
     const size_t lead = rows.size();
     if (lead != (bsnd ? 2u : 1u) || (!bsnd && !cu_k)) refuse("scores must be [B,S2], or [T2] with cu_seqlens_k");
-    if (budget < 1 || caches.size() > SLIKL_EVICT_MAX_CACHES)
-        refuse("budget must be at least 1, and caches at most ", SLIKL_EVICT_MAX_CACHES);
+    if (budget < 1 || budget >> 31 || caches.size() > SLIKL_EVICT_MAX_CACHES)
+        refuse("budget must be at least 1 and below 2^31, and caches at most ", SLIKL_EVICT_MAX_CACHES);
     if (out_caches && out_caches->size() != caches.size()) refuse("out['caches'] must have a tensor for each cache");
-    const c10::cuda::OptionalCUDAGuard guard(dev);
+    const On on(dev, stream);
     slikl_evict_problem pr{};
     slikl_evict_tensors tn{};
     pr.layout_k = layout_k;
@@ -405,8 +430,15 @@ py::tuple evict(Tensor scores, std::vector<Tensor> caches, int64_t budget, int64
     tn.seq_used_k = lengths(used_k, "seq_used_k", dev, pr.B);
     const int64_t one[1] = {1}, batch[1] = {pr.B}, places[2] = {pr.B, budget};
     if (status) tn.status = address<uint32_t>(*status, "status", dev, at::kInt, at::IntArrayRef(one));
-    Tensor kept = out_kept ? *out_kept : fresh(places, at::kInt, dev);
-    Tensor lens = out_lengths ? *out_lengths : fresh(batch, at::kInt, dev);
+    Tensor kept, lens;
+    if (!out_kept && !out_lengths && pr.B >= 0) {     // one allocation for both
+        const Tensor both = fresh({pr.B * (budget + 1)}, at::kInt, dev);
+        kept = part_of(both, 0, places);
+        lens = part_of(both, pr.B * budget, batch);
+    } else {
+        kept = out_kept ? *out_kept : fresh(places, at::kInt, dev);
+        lens = out_lengths ? *out_lengths : fresh(batch, at::kInt, dev);
+    }
     Tensor best = out_scores ? *out_scores : fresh(places, at::kFloat, dev);
     tn.kept = address<int32_t>(kept, "kept", dev, at::kInt, at::IntArrayRef(places));
     tn.lengths = address<int32_t>(lens, "lengths", dev, at::kInt, at::IntArrayRef(batch));
