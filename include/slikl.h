@@ -439,8 +439,8 @@ SLIKL_API slikl_status slikl_grad_recompute_p(const slikl_problem *problem,
  * then, for the first rot_dim dims, y = z turned by the row's angles, (a, b) ->
  * (a cos - b sin, b cos + a sin), where (a, b) are dims (i, i + rot_dim/2) (SLIKL_ROT_HALVES) or
  * (2i, 2i + 1) (SLIKL_ROT_PAIRS), i < rot_dim/2; the other dims are y = z. Sums are fp32, and y is
- * rounded once to the 16-bit type. (A bf16 x whose squares overflow fp32, |x| above about 1e18,
- * is outside the norms' range.)
+ * rounded once to the 16-bit type. (A head's row with an infinity, or with a bf16 x whose squares overflow
+ * fp32, |x| above about 1e18, is outside the norms' range: its y and dx may be NaN in every dim.)
  *
  * The gradient, with dz = dy turned back and xhat = (x - m) r (m = 0 for RMS):
  *   dgain = sum dz xhat, dbias = sum dz   (over all heads of all rows; fp32, the same bits each call)

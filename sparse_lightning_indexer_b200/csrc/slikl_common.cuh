@@ -181,11 +181,12 @@ slikl_status check_index_call(const slikl_problem *problem, const slikl_tensors 
 // await_previous() before it touches memory (it returns when the earlier kernel has ended and its
 // writes are visible).
 template <typename... P, typename... A>
-inline cudaError_t launch_next(void (*kernel)(P...), dim3 grid, unsigned threads, cudaStream_t s,
+inline cudaError_t launch_next(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t s,
                                const A &...args) {
     cudaLaunchConfig_t c{};
     c.gridDim = grid;
     c.blockDim = dim3(threads);
+    c.dynamicSmemBytes = smem;
     c.stream = s;
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;

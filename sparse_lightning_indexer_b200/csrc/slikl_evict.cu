@@ -393,7 +393,7 @@ slikl_status slikl_evict(const slikl_evict_problem *problem, const slikl_evict_t
     if (cudaGetLastError() != cudaSuccess) return SLIKL_ERR_CUDA;
     if (p.n_caches > 0) {
         const dim3 grid((unsigned)blocks, (unsigned)p.n_caches, (unsigned)std::min<int64_t>(p.B, 65535));
-        if (launch_next(evict_copy, grid, kCopy, s, a) != cudaSuccess) return SLIKL_ERR_CUDA;
+        if (launch_next(evict_copy, grid, kCopy, 0, s, a) != cudaSuccess) return SLIKL_ERR_CUDA;
     }
     return SLIKL_OK;
 }

@@ -226,6 +226,13 @@ __global__ void __launch_bounds__(kDirectThreads) weights_direct(WeightArgs a, i
     }
 }
 
+// A kernel instead of a memset: weights_split starts while it runs.
+__global__ void __launch_bounds__(512) weights_clear(ulonglong2 *sums, int64_t pairs) {
+    let_next_start();         // weights_split, weights_finish
+    for (int64_t i = (int64_t)blockIdx.x * 512 + threadIdx.x; i < pairs; i += (int64_t)gridDim.x * 512)
+        sums[i] = make_ulonglong2(0, 0);
+}
+
 // grid (chunks of keys, splits of the slots, batches). Blocks next to one another read the same slots.
 __global__ void __launch_bounds__(kSplitThreads) weights_split(WeightArgs a, int chunk) {
     extern __shared__ uint32_t low[];
@@ -234,12 +241,12 @@ __global__ void __launch_bounds__(kSplitThreads) weights_split(WeightArgs a, int
     const int64_t slots = r.end - r.begin;
     const int64_t begin = r.begin + slots * blockIdx.y / gridDim.y;
     const int64_t end = r.begin + slots * (blockIdx.y + 1) / gridDim.y;
-    if (begin == end) return;
-    for (int64_t first = (int64_t)blockIdx.x * chunk; first < r.used;
+    for (int64_t first = (int64_t)blockIdx.x * chunk; begin < end && first < r.used;
          first += (int64_t)gridDim.x * chunk) {
         const int32_t keys = (int32_t)min((int64_t)chunk, r.used - first);
         unsigned long long *sums = a.sums + r.base + first;
         for (int i = threadIdx.x; i < keys; i += kSplitThreads) low[i] = 0;
+        await_previous();     // carries go to the sums
         __syncthreads();
         const auto more = [&](uint32_t k, uint32_t n) { atomicAdd(sums + k, (unsigned long long)n << 32); };
         add_some<kSplitThreads>(a, r, begin, end, (int32_t)first, keys, low, more);
@@ -248,6 +255,7 @@ __global__ void __launch_bounds__(kSplitThreads) weights_split(WeightArgs a, int
             if (low[i]) atomicAdd(sums + i, (unsigned long long)low[i]);
         __syncthreads();
     }
+    await_previous();         // for blocks without slots too: weights_finish waits for this kernel alone
 }
 
 __global__ void __launch_bounds__(256) weights_finish(WeightArgs a) {
@@ -371,8 +379,10 @@ slikl_status slikl_key_weights(const slikl_problem *problem,
         weights_direct<<<dim3((unsigned)chunks, (unsigned)pr.B), kDirectThreads, 0, s>>>(a, (int)chunk);
         return cudaGetLastError() == cudaSuccess ? SLIKL_OK : SLIKL_ERR_CUDA;
     }
-    if (cudaMemsetAsync(a.sums, 0, sizeof(*a.sums) * (size_t)T2, s) != cudaSuccess)
-        return SLIKL_ERR_CUDA;
+    const int64_t pairs = (T2 + 1) / 2;
+    weights_clear<<<(unsigned)std::min<int64_t>((pairs + 511) / 512, 2 * sms), 512, 0, s>>>(
+        reinterpret_cast<ulonglong2 *>(a.sums), pairs);
+    if (cudaGetLastError() != cudaSuccess) return SLIKL_ERR_CUDA;
     if (T1 > 0) {
         const int64_t chunks = (range + kSplitKeys - 1) / kSplitKeys;
         const int64_t chunk = (range + chunks - 1) / chunks;
@@ -387,15 +397,13 @@ slikl_status slikl_key_weights(const slikl_problem *problem,
         // the grid's third dimension holds 65535 batches
         for (int64_t b = 0; b < pr.B; b += 65535) {
             part.first_batch = b;
-            weights_split<<<dim3((unsigned)chunks, (unsigned)splits, (unsigned)std::min<int64_t>(pr.B - b, 65535)),
-                     kSplitThreads, smem, s>>>(part, (int)chunk);
-            if (cudaGetLastError() != cudaSuccess) return SLIKL_ERR_CUDA;
+            const dim3 grid((unsigned)chunks, (unsigned)splits, (unsigned)std::min<int64_t>(pr.B - b, 65535));
+            if (launch_next(weights_split, grid, kSplitThreads, smem, s, part, (int)chunk) != cudaSuccess)
+                return SLIKL_ERR_CUDA;
         }
     }
     const dim3 grid((unsigned)((T2 + 255) / 256));
-    if (T1 > 0) return launch_next(weights_finish, grid, 256, s, a) == cudaSuccess ? SLIKL_OK : SLIKL_ERR_CUDA;
-    weights_finish<<<grid, 256, 0, s>>>(a);
-    return cudaGetLastError() == cudaSuccess ? SLIKL_OK : SLIKL_ERR_CUDA;
+    return launch_next(weights_finish, grid, 256, 0, s, a) == cudaSuccess ? SLIKL_OK : SLIKL_ERR_CUDA;
 }
 
 }  // extern "C"

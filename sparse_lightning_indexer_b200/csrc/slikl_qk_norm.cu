@@ -1055,7 +1055,7 @@ slikl_status run_gradient(const slikl_qk_problem *p, const slikl_qk_tensors *t, 
               {a.blocks_q, a.blocks_q, a.blocks_k, a.blocks_k},
               partial, (int)p->D};
     if (sums.out[0] || sums.out[1] || sums.out[2] || sums.out[3]) {
-        if (launch_next(qk_grad_sums, dim3((unsigned)p->D / 32, 4), 1024, st, sums) != cudaSuccess)
+        if (launch_next(qk_grad_sums, dim3((unsigned)p->D / 32, 4), 1024, 0, st, sums) != cudaSuccess)
             return SLIKL_ERR_CUDA;
     }
     return SLIKL_OK;
