@@ -192,6 +192,43 @@ def test_key_weights_beyond_one_pass_of_p():
     assert r[0, 17] == T and r.sum() == T
 
 
+def test_more_sequences_than_a_grid_dimension_holds():
+    """66000 sequences of a few rows: weights over all of them, and their caches cut."""
+    B, S2, K = 66000, 5, 3
+    idx, w = draw_rows(31, [1] * B, [S2] * B, K)
+    scores = torch.rand(B * S2, generator=torch.Generator().manual_seed(32))
+    r = sli.key_weights(dev(w).view(B, 1, 1, K), dev(idx).view(B, 1, 1, K), dev(scores).view(B, S2), decay=0.5)
+    rows = torch.where(idx >= 0, idx + S2 * torch.arange(B)[:, None], 0).reshape(-1).long()
+    full = torch.where(idx >= 0, w, 0.0).double().reshape(-1)
+    want = 0.5 * scores.double() + torch.bincount(rows, weights=full, minlength=B * S2)
+    named = torch.bincount(rows, minlength=B * S2)
+    got = r["scores"].cpu().double().reshape(-1)
+    assert ((got - want).abs() <= weights_bound(want, named, idx.numel(), scores)).all()
+    c = torch.randn(B, S2, 8, device="cuda").to(torch.bfloat16)
+    cut = sli.evict(r["scores"], [c], 2, recent=1)
+    order = r["scores"].clone()
+    order[:, -1] = float("inf")
+    keep = order.sort(dim=1, descending=True, stable=True).indices[:, :2].sort(1).values
+    assert torch.equal(cut["kept"].long(), keep) and (cut["lengths"] == 2).all()
+    assert torch.equal(cut["caches"][0], c.gather(1, keep[..., None].expand(-1, -1, 8)))
+
+
+def test_key_weights_calls_in_flight_on_two_streams():
+    """Calls of several launches each, behind one another and beside each other, with workspaces of their own."""
+    sets = []
+    for seed in (41, 42):
+        idx, w = draw_rows(seed, [700], [9000], 300)
+        sets.append((dev(w).view(1, 700, 1, 300), dev(idx).view(1, 700, 1, 300), torch.rand(1, 9000, device="cuda")))
+    want = [sli.key_weights(*a)["scores"] for a in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    ws = [sli.key_weights(*a)["workspace"] for a in sets]
+    torch.cuda.synchronize()
+    got = [[sli.key_weights(*a, workspace=k, stream=st)["scores"] for a, k, st in zip(sets, ws, streams)] for _ in range(30)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, v) for turn in got for g, v in zip(turn, want))
+
+
 def test_key_weights_without_queries_or_keys():
     e = torch.empty(0, 1, 8, device="cuda")
     s = torch.rand(30, device="cuda")
