@@ -623,7 +623,7 @@ typedef struct {
 
 typedef struct {
     const void *in;          /* device, 16-byte aligned */
-    void *out;               /* device, 16-byte aligned; no overlap with any input or output */
+    void *out;               /* device, 16-byte aligned */
     int64_t row_bytes;       /* bytes of one key row, a positive multiple of 16 */
 } slikl_evict_cache;
 
@@ -632,15 +632,17 @@ typedef struct {
     const int32_t *cu_seqlens_k;    /* int32 [B+1], TND only, else NULL                          */
     const int32_t *seq_used_k;      /* int32 [B] rows in use, or NULL: all                       */
     int32_t *kept;                  /* out int32 [B][budget]                                     */
-    int32_t *lengths;               /* out int32 [B]                                             */
-    float *scores_out;              /* out fp32  [B][budget], or NULL; not scores itself         */
+    int32_t *lengths;               /* out int32 [B]; may be seq_used_k itself                    */
+    float *scores_out;              /* out fp32  [B][budget], or NULL                            */
     uint32_t *status;               /* optional device word: the call ORs SLIKL_DEV_BAD_CU_SEQLENS_K
                                        and SLIKL_DEV_BAD_SEQ_USED in                             */
     slikl_evict_cache caches[SLIKL_EVICT_MAX_CACHES];
 } slikl_evict_tensors;
 
-/* Needs no workspace. Errors: SLIKL_ERR_PARAM_NULLPTR, SLIKL_ERR_PARAM_INVALID (values outside the
- * sets above, misaligned or overlapping pointers), SLIKL_ERR_CUDA. */
+/* Needs no workspace. No output, the status word among them, may share memory with an input or with
+ * another output (lengths in place of seq_used_k apart).
+ * Errors: SLIKL_ERR_PARAM_NULLPTR, SLIKL_ERR_PARAM_INVALID (values outside the sets above, misaligned
+ * or overlapping pointers), SLIKL_ERR_CUDA. */
 SLIKL_API slikl_status slikl_evict(const slikl_evict_problem *problem,
                                    const slikl_evict_tensors *tensors, void *stream);
 

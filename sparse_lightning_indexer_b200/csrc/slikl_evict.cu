@@ -243,6 +243,8 @@ __global__ void __launch_bounds__(kChoose) __cluster_dims__(CS, 1, 1) evict_choo
         kept[j] = -1;
         if (out) out[j] = 0.f;
     }
+    if (CS == 1) __syncthreads();         // every thread has read seq_used_k, which lengths may be (a
+                                          // cluster has met above)
     if (threadIdx.x == 0 && rank == 0) a.lengths[b] = (int32_t)stay;
     if (CS > 1) cluster.sync();           // the others may still read this block's counts
 }
@@ -295,9 +297,15 @@ __global__ void __launch_bounds__(kCopy) evict_copy(EvictArgs a) {
 
 bool misaligned(const void *p, uintptr_t to) { return reinterpret_cast<uintptr_t>(p) & (to - 1); }
 
-bool overlap(const void *p, int64_t n, const void *q, int64_t m) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(p), y = reinterpret_cast<uintptr_t>(q);
-    return n > 0 && m > 0 && x < y + (uint64_t)m && y < x + (uint64_t)n;
+// Bytes of one tensor; none where the pointer is null.
+struct Range {
+    const void *p;
+    int64_t n;
+};
+
+bool overlap(const Range &r, const Range &q) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(r.p), y = reinterpret_cast<uintptr_t>(q.p);
+    return r.p && q.p && r.n > 0 && q.n > 0 && x < y + (uint64_t)q.n && y < x + (uint64_t)r.n;
 }
 
 }  // namespace
@@ -332,9 +340,6 @@ slikl_status slikl_evict(const slikl_evict_problem *problem, const slikl_evict_t
         misaligned(t.kept, 4) || misaligned(t.lengths, 4) || misaligned(t.scores_out, 4) ||
         misaligned(t.status, 4))
         return SLIKL_ERR_PARAM_INVALID;
-    const int64_t places = p.B * p.budget;
-    if (t.scores_out && overlap(t.scores, T2 * 4, t.scores_out, places * 4))
-        return SLIKL_ERR_PARAM_INVALID;
     for (int i = 0; i < p.n_caches; ++i) {
         const slikl_evict_cache &c = t.caches[i];
         if (c.row_bytes < 16 || c.row_bytes % 16 != 0 || c.row_bytes >= limit)
@@ -342,16 +347,24 @@ slikl_status slikl_evict(const slikl_evict_problem *problem, const slikl_evict_t
         if ((T2 > 0 && !c.in) || !c.out) return SLIKL_ERR_PARAM_NULLPTR;
         if (misaligned(c.in, 16) || misaligned(c.out, 16)) return SLIKL_ERR_PARAM_INVALID;
     }
-    // rows are copied while others are still to be read: nothing written may lie in an input, and
-    // no two outputs may share memory
+    // Scores, lengths and rows are read while others are written, and evict_copy follows the row numbers
+    // of `kept` wherever they lead: nothing written may lie in an input or in another output. (A
+    // sequence's length is written behind the last read of its used length.)
+    const int64_t places = p.B * p.budget;
+    Range in[3 + SLIKL_EVICT_MAX_CACHES] = {{t.scores, T2 * 4},
+                                            {p.layout_k == SLIKL_TND ? t.cu_seqlens_k : nullptr, (p.B + 1) * 4},
+                                            {t.lengths == t.seq_used_k ? nullptr : t.seq_used_k, p.B * 4}};
+    Range out[4 + SLIKL_EVICT_MAX_CACHES] = {{t.kept, places * 4}, {t.lengths, p.B * 4},
+                                             {t.scores_out, places * 4}, {t.status, 4}};
     for (int i = 0; i < p.n_caches; ++i) {
-        const slikl_evict_cache &c = t.caches[i];
-        for (int j = 0; j < p.n_caches; ++j) {
-            const slikl_evict_cache &d = t.caches[j];
-            if (overlap(c.out, places * c.row_bytes, d.in, T2 * d.row_bytes) ||
-                (i != j && overlap(c.out, places * c.row_bytes, d.out, places * d.row_bytes)))
-                return SLIKL_ERR_PARAM_INVALID;
-        }
+        in[3 + i] = {t.caches[i].in, T2 * t.caches[i].row_bytes};
+        out[4 + i] = {t.caches[i].out, places * t.caches[i].row_bytes};
+    }
+    for (int i = 0; i < 4 + p.n_caches; ++i) {
+        for (int j = 0; j < 3 + p.n_caches; ++j)
+            if (overlap(out[i], in[j])) return SLIKL_ERR_PARAM_INVALID;
+        for (int j = 0; j < i; ++j)
+            if (overlap(out[i], out[j])) return SLIKL_ERR_PARAM_INVALID;
     }
     int dev = 0, major = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||

@@ -321,6 +321,17 @@ def test_evict_without_caches_and_default_outputs():
     assert torch.equal(r["caches"][0][0, :3], c[0, :3]) and (r["caches"][0][0, 3:] == 0).all()
 
 
+@pytest.mark.parametrize("S2", [60, 3000, 20000])
+def test_evict_lengths_in_place(S2):
+    """The used lengths may become the kept ones in place."""
+    s = torch.rand(4, S2, device="cuda")
+    used = torch.tensor([0, 7, S2, S2 // 2], dtype=torch.int32, device="cuda")
+    want = sli.evict(s, [], 20, sinks=1, recent=2, seq_used_k=used.clone())
+    got = sli.evict(s, [], 20, sinks=1, recent=2, seq_used_k=used, out=dict(lengths=used))
+    assert used.tolist() == [0, 7, 20, 20] and torch.equal(got["kept"], want["kept"])
+    assert torch.equal(got["scores"], want["scores"])
+
+
 def test_evict_flags():
     s = torch.rand(3, 20, device="cuda")
     status = torch.zeros(1, dtype=torch.int32, device="cuda")

@@ -291,6 +291,56 @@ def test_evict_tensors_refused(lib):
     assert passes(evict_rc, lib, pr, tn)
 
 
+def test_evict_refuses_outputs_over_other_tensors(lib):
+    """The rows of `kept` are followed wherever they lead, and scores are read while rows are chosen: no
+    output may share a byte with an input or with another output, whichever they are."""
+    def call(tnd):
+        pr, tn = evict_call()
+        tn.seq_used_k = 0x60000
+        if tnd:
+            pr.layout_k, pr.S2, pr.T2, tn.cu_seqlens_k = sli.SLIKL_TND, 0, 200, 0x70000
+        return pr, tn
+
+    outs = {"kept": 80, "lengths": 8, "scores_out": 80, "status": 4, 0: 20 * 256, 1: 20 * 16}
+    ins = {"scores": 800, "seq_used_k": 8, "cu_seqlens_k": 12, 0: 200 * 256, 1: 200 * 16}
+
+    def at(tn, name, out):
+        if isinstance(name, str):
+            return getattr(tn, name)
+        return tn.caches[name].out if out else tn.caches[name].in_
+
+    def move(tn, name, to):
+        if isinstance(name, str):
+            setattr(tn, name, to)
+        else:
+            tn.caches[name].out = to
+
+    for tnd in (False, True):
+        assert passes(evict_rc, lib, *call(tnd))
+        for o, size in outs.items():
+            step = 4 if isinstance(o, str) else 16           # keeps it aligned
+            others = [(n, s, True) for n, s in outs.items() if n != o] + [(n, s, False) for n, s in ins.items()]
+            for name, n, is_out in others:
+                if name == "cu_seqlens_k" and not tnd:
+                    continue                                 # not there
+                pr, tn = call(tnd)
+                there = at(tn, name, is_out)
+                last = (there + n - 1) // step * step        # shares the last bytes, shares the first ones
+                first = there - (size - 1) // step * step
+                for to in (there, last, first):
+                    if (o, name, to) == ("lengths", "seq_used_k", there):
+                        continue                             # allowed: in place
+                    pr, tn = call(tnd)
+                    move(tn, o, to)
+                    assert evict_rc(lib, pr, tn) == INVALID, (o, name, hex(to))
+        pr, tn = call(tnd)
+        tn.lengths = tn.seq_used_k
+        assert passes(evict_rc, lib, pr, tn)
+        pr, tn = call(tnd)                                   # next to one another is not over one another
+        tn.lengths, tn.scores_out = tn.kept + 80, tn.kept + 88
+        assert passes(evict_rc, lib, pr, tn)
+
+
 def test_binding_refuses_before_any_launch():
     """Wrong types, shapes and devices raise ValueError, on the CPU too."""
     x = torch.zeros(1, 4, 2, 64, dtype=torch.bfloat16)
