@@ -545,7 +545,9 @@ SLIKL_API slikl_status slikl_qk_norm_rope_grad(const slikl_qk_problem *problem,
  * dq and dk, and y, keep8, dy and status of qk_tensors, are not looked at. Same streams, workspace
  * and status-word rules as slikl_grad_ex, whose status word also receives SLIKL_DEV_BAD_POSITION.
  * A padding row's q or k is 0 here (its position is -1), which leaves it to sparse_indices and the
- * used lengths to keep the row out of the loss.
+ * used lengths to keep the row out of the loss. Rows behind seq_used_q / seq_used_k are padding rows,
+ * whatever position they have: their x may hold anything, their dx is 0 and they take no part in
+ * dgain and dbias.
  * Errors: those of the three calls.
  */
 SLIKL_API slikl_status slikl_grad_projected_workspace_size(const slikl_problem *problem,

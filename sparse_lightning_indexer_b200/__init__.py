@@ -838,8 +838,9 @@ def grad_projected(x_q, x_k, w, attn_softmax_l1norm, sparse_indices, cos_sin=Non
                    seq_used_k=None, stream=None):
     """grad() from the outputs of the projections, or from their checkpoints: q and k as
     qk_norm_rope forms them, the indexer's gradient, and dq, dk back as qk_norm_rope_grad takes
-    them, in one call (slikl_grad_projected). Returns dict(dx_q, dx_k, dgain_*, dbias_*, dw,
-    softmax_out, workspace[, loss]); `out` may supply dx_q / dx_k."""
+    them, in one call (slikl_grad_projected). Rows behind the used lengths are padding: their x may
+    hold anything, and their dx is 0. Returns dict(dx_q, dx_k, dgain_*, dbias_*, dw, softmax_out,
+    workspace[, loss]); `out` may supply dx_q / dx_k."""
     if x_q is None or x_k is None:
         raise ValueError("x_q and x_k are both needed")
     out_q, out_k = (out.get("dx_q"), out.get("dx_k")) if out else (None, None)

@@ -859,6 +859,36 @@ __global__ void __launch_bounds__(1024) qk_grad_sums(Sums a) {
     }
 }
 
+// Positions of the rows of a slikl_grad_projected call with used lengths: those that the caller gives (or t
+// % S), and -1 for the rows behind a batch's used ones, whose x, like the gradient's own padding rows, may
+// hold anything: without a position a NaN there would reach dgain as 0 * NaN.
+struct UsedRows {
+    int64_t T, S, batch, B;   // rows; S of slikl_qk_side; rows of a batch (0: cu), batches
+    const int32_t *cu, *used, *positions;
+    int32_t *out;             // null: this side has no used lengths
+};
+
+__global__ void __launch_bounds__(256) used_positions(UsedRows q, UsedRows k) {
+    const UsedRows &s = blockIdx.y ? k : q;
+    const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (!s.out || t >= s.T) return;
+    int64_t b, local;
+    if (s.batch) {
+        b = t / s.batch;
+        local = t - b * s.batch;
+    } else {                  // the last batch that starts at t or before
+        int64_t lo = 0, hi = s.B;
+        while (hi - lo > 1) {
+            const int64_t mid = (lo + hi) / 2;
+            if (s.cu[mid] <= t) lo = mid;
+            else hi = mid;
+        }
+        b = lo;
+        local = t - s.cu[b];
+    }
+    s.out[t] = local >= s.used[b] ? -1 : s.positions ? s.positions[t] : (int32_t)(t % s.S);
+}
+
 // --- host side ---------------------------------------------------------------------------------
 
 bool misaligned(const void *p, uintptr_t to) { return reinterpret_cast<uintptr_t>(p) & (to - 1); }
@@ -1065,10 +1095,10 @@ size_t grad_workspace(const slikl_qk_problem *p) {
     return align256(sizeof(float) * 4 * kGradBlocks * (size_t)p->D);
 }
 
-// slikl_grad_projected's workspace: slikl_grad_ex's (its status word first), then q, k, dq, dk,
-// then the gradient's partial sums.
+// slikl_grad_projected's workspace: slikl_grad_ex's (its status word first), then q, k, dq, dk, the
+// rows' positions (where there are used lengths), then the gradient's partial sums.
 struct ProjectedLayout {
-    size_t q, k, dq, dk, partial, total;
+    size_t q, k, dq, dk, pos_q, pos_k, partial, total;
 };
 
 slikl_status check_projected(const slikl_problem *pr, const slikl_qk_problem *qk,
@@ -1088,7 +1118,9 @@ slikl_status check_projected(const slikl_problem *pr, const slikl_qk_problem *qk
     L->k = L->q + qb;
     L->dq = L->k + kb;
     L->dk = L->dq + qb;
-    L->partial = L->dk + kb;
+    L->pos_q = L->dk + kb;
+    L->pos_k = L->pos_q + align256(sizeof(int32_t) * (size_t)T1);
+    L->partial = L->pos_k + align256(sizeof(int32_t) * (size_t)T2);
     L->total = L->partial + grad_workspace(qk);
     return SLIKL_OK;
 }
@@ -1183,6 +1215,22 @@ slikl_status slikl_grad_projected(const slikl_problem *problem, const slikl_qk_p
     const int sms = sm100_multiprocessors();
     if (!sms) return SLIKL_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (options && (options->seq_used_q || options->seq_used_k)) {
+        auto rows = [&](const slikl_qk_side &side, slikl_qk_side_tensors &t, const int32_t *used, int layout,
+                        int64_t batch, const int32_t *cu, size_t at) {
+            UsedRows u{side.T, std::max<int64_t>(1, side.S), layout == SLIKL_BSND ? batch : 0, problem->B, cu, used,
+                       t.positions, nullptr};
+            if (used && side.T > 0) t.positions = u.out = reinterpret_cast<int32_t *>(ws + at);
+            return u;
+        };
+        const UsedRows uq = rows(qk->q, qt.q, options->seq_used_q, problem->layout_q, problem->S1, tn.cu_seqlens_q, L.pos_q);
+        const UsedRows uk = rows(qk->k, qt.k, options->seq_used_k, problem->layout_k, problem->S2, tn.cu_seqlens_k, L.pos_k);
+        const int64_t most = std::max(uq.out ? uq.T : 0, uk.out ? uk.T : 0);
+        if (most > 0) {
+            used_positions<<<dim3((unsigned)((most + 255) / 256), 2), 256, 0, s>>>(uq, uk);
+            if (cudaGetLastError() != cudaSuccess) return SLIKL_ERR_CUDA;
+        }
+    }
     st = run_forward(qk, &qt, sms, s);
     if (st != SLIKL_OK) return st;
     st = slikl_grad_ex(problem, &tn, workspace, L.q, stream, options);

@@ -506,6 +506,58 @@ def test_projected_gradient(layout, source, mode):
     assert sli.slikl_read_device_status(res["workspace"].data_ptr()) == sli.SLIKL_DEV_BAD_POSITION
 
 
+@pytest.mark.parametrize("layout,positions", [("BSND", True), ("BSND", False), ("TND", True)])
+@pytest.mark.parametrize("source", ["x", "x8"])
+def test_projected_gradient_of_a_padded_batch(layout, positions, source):
+    """Rows behind the used lengths hold NaN: everything is as with zeros at position -1 in their place,
+    bit by bit, and their dx is 0."""
+    B, S1, S2, N1, D, K, R = 3, 30, 200, 16, 128, 64, 64
+    wl = si.small(seed=75, layout=layout, B=B, S1=S1, S2=S2, N1=N1, D=D, K=K)
+    dtype = wl.q.dtype
+    cuq, cuk = ([0, S1, 2 * S1, 3 * S1], [0, S2, 2 * S2, 3 * S2]) if layout == "BSND" else (
+        wl.cu_seqlens_q.tolist(), wl.cu_seqlens_k.tolist())
+    B, T1, T2 = len(cuq) - 1, wl.T1, wl.T2
+    used_q = [max(0, (cuq[b + 1] - cuq[b]) * (2 - b) // 2) for b in range(B)]      # all, half, none
+    used_k = [max(1, (cuk[b + 1] - cuk[b]) * (b + 1) // B) for b in range(B)]
+    q, k = make(76, T1, N1, D, R, dtype, "layer"), make(77, T2, 1, D, R, dtype, "rms")
+    cs, pad, pos, x = table(400, R), {}, {}, {}
+    for n, s, cu, used in (("q", q, cuq, used_q), ("k", k, cuk, used_k)):
+        local = torch.cat([torch.arange(cu[b + 1] - cu[b]) for b in range(B)])
+        pad[n] = torch.cat([torch.arange(cu[b + 1] - cu[b]) >= used[b] for b in range(B)])
+        pos[n] = (local + 100 if positions else local).to(torch.int32)
+        x[n] = s["x"].clone()
+        x[n][pad[n]] = 0
+    assert pad["q"].any() and pad["k"].any()
+    shape = dict(q=wl.q.shape, k=wl.k.shape)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    kw = dict(gain_q=dev(q["gain"] * 0.1), gain_k=dev(k["gain"]), bias_q=dev(q["bias"]), norm_q="layer",
+              layout_q=layout, layout_k=layout, deterministic=True, loss=True,
+              cu_seqlens_q=dev(wl.cu_seqlens_q), cu_seqlens_k=dev(wl.cu_seqlens_k),
+              key_range_bound=sli.key_range_bound_of(wl), seq_used_q=torch.tensor(used_q, **i32),
+              seq_used_k=torch.tensor(used_k, **i32))
+
+    def run(x, **pos):
+        xs = [dev(x[n]).reshape(shape[n]) for n in "qk"]
+        if source == "x8":
+            xs = [sli.checkpoint_pack(t) for t in xs]
+        r = sli.grad_projected(*xs, dev(wl.w), dev(wl.p), dev(wl.idx), dev(cs), **pos, **kw)
+        torch.cuda.synchronize()
+        assert sli.slikl_read_device_status(r.pop("workspace").data_ptr()) == 0
+        return r
+
+    want = run(x, **{"pos_" + n: dev(torch.where(pad[n], -1, pos[n])) for n in "qk"})
+    for n in "qk":
+        x[n][pad[n]] = float("nan")
+        pos[n][pad[n]] = 1 << 30                 # no position either
+    got = run(x, **({"pos_" + n: dev(pos[n]) for n in "qk"} if positions else {}))
+    for n, v in want.items():
+        assert (got[n] is None) == (v is None) and (v is None or torch.equal(got[n], v)), n
+    for n in "qk":
+        assert torch.isfinite(got["dgain_" + n]).all() and got["dgain_" + n].abs().sum() > 0
+        dx = got["dx_" + n].reshape(-1, N1 if n == "q" else 1, D)
+        assert (dx[pad[n].cuda()] == 0).all() and torch.isfinite(dx).all()
+
+
 @pytest.mark.parametrize("T1,T2", [(0, 40), (30, 0)])
 def test_projected_gradient_without_queries_or_keys(T1, T2):
     """Empty TND sides: what is there gets zero gradients."""
