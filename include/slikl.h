@@ -570,7 +570,8 @@ SLIKL_API slikl_status slikl_grad_projected(const slikl_problem *problem,
  * with weights the attention of the call's query rows over their slots (attn_softmax_l1norm,
  * softmax_out, or the p of slikl_grad_recompute_p). Layouts, used lengths and valid slots are
  * slikl_grad's; dtype, N1, D and deterministic of the problem are not read. Every key row is
- * written (unused ones as decay * scores). With decay = 0 scores is not read.
+ * written (unused ones as decay * scores; all of them so where SLIKL_DEV_BAD_CU_SEQLENS_K is set, which
+ * empties the batches' key ranges). With decay = 0 scores is not read.
  *
  * Weights are summed as 64-bit integers in units of 2^-u, u = min(40, 61 - ceil(log2(T1 * topk))),
  * so the result has the same bits whatever the order; each weight is rounded to a multiple of

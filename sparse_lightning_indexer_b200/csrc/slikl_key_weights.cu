@@ -37,6 +37,7 @@ struct WeightArgs {
     float decay;
     float one;                // 2^u: the units of a weight of 1
     unsigned long long *sums; // [T2], in units
+    uint32_t *bad_k;          // weights_clear's finding that cu_seqlens_k is unusable; null: BSND keys
     int64_t first_batch;      // of weights_split's grid
     uint32_t *status;
 };
@@ -130,6 +131,18 @@ __device__ __forceinline__ void add_four(const WeightArgs &a, const uint32_t *v,
     }
 }
 
+// Whether this thread sees cu_seqlens_k break its contract (0 .. T2, non-decreasing). All batches' key ranges
+// are empty then, as in the gradient: ranges that overlap or leave rows out have no meaning.
+__device__ __forceinline__ bool sees_bad_keys(const WeightArgs &a) {
+    bool bad = false;
+#pragma unroll 4
+    for (int64_t b = threadIdx.x; b < a.B; b += blockDim.x) {
+        const int64_t k0 = a.cu_k[b], k1 = a.cu_k[b + 1];
+        bad |= k1 < k0 || (b == 0 && k0 != 0) || (b == a.B - 1 && k1 != a.T2);
+    }
+    return bad;
+}
+
 // Adds the slots of [begin, end) that name a key of [first, first + keys) to the low words. Flags
 // indices that break the contract. A step is four slots a thread, a block's width apart; loads run
 // ahead, the indices two steps and the weights, read only where the slot counts, one.
@@ -211,6 +224,12 @@ __global__ void __launch_bounds__(kDirectThreads) weights_direct(WeightArgs a, i
     const int64_t b = blockIdx.y;
     if (blockIdx.x == 0 && b == 0 && a.status) check_batches(a);
     const Batch r = batch_of(a, b);
+    if (a.layout_k == SLIKL_TND && __syncthreads_or(sees_bad_keys(a))) {
+        const int64_t blocks = (int64_t)gridDim.x * gridDim.y, mine = b * gridDim.x + blockIdx.x;
+        for (int64_t key = mine * kDirectThreads + threadIdx.x; key < a.T2; key += blocks * kDirectThreads)
+            a.out[key] = finished(a, 0, key);
+        return;
+    }
     for (int64_t first = (int64_t)blockIdx.x * chunk; first < r.count;
          first += (int64_t)gridDim.x * chunk) {
         const int32_t keys = (int32_t)min((int64_t)chunk, r.count - first);
@@ -228,10 +247,15 @@ __global__ void __launch_bounds__(kDirectThreads) weights_direct(WeightArgs a, i
 }
 
 // A kernel instead of a memset: weights_split starts while it runs.
-__global__ void __launch_bounds__(512) weights_clear(ulonglong2 *sums, int64_t pairs) {
+__global__ void __launch_bounds__(512) weights_clear(WeightArgs a, int64_t pairs) {
     let_next_start();         // weights_split, weights_finish
+    ulonglong2 *sums = reinterpret_cast<ulonglong2 *>(a.sums);
     for (int64_t i = (int64_t)blockIdx.x * 512 + threadIdx.x; i < pairs; i += (int64_t)gridDim.x * 512)
         sums[i] = make_ulonglong2(0, 0);
+    if (a.bad_k && blockIdx.x == 0) {
+        const int bad = __syncthreads_or(sees_bad_keys(a));
+        if (threadIdx.x == 0) *a.bad_k = bad != 0;
+    }
 }
 
 // grid (chunks of keys, splits of the slots, batches). Blocks next to one another read the same slots.
@@ -263,7 +287,8 @@ __global__ void __launch_bounds__(256) weights_finish(WeightArgs a) {
     await_previous();
     if (blockIdx.x == 0 && a.status) check_batches(a);
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i < a.T2) a.out[i] = finished(a, a.sums[i], i);
+    const bool none = a.bad_k && *a.bad_k;
+    if (i < a.T2) a.out[i] = finished(a, none ? 0 : a.sums[i], i);
 }
 
 // --- host side ---------------------------------------------------------------------------------
@@ -279,13 +304,14 @@ slikl_problem index_problem(const slikl_problem &p) {
 }
 
 struct Layout {
-    size_t sums, total;
+    size_t sums, bad_k, total;
 };
 
 Layout make_workspace(int64_t T2) {
     Layout L;
     L.sums = 0;
-    L.total = align256(sizeof(unsigned long long) * (size_t)T2) + 256;
+    L.bad_k = align256(sizeof(unsigned long long) * (size_t)T2);
+    L.total = L.bad_k + 256;
     return L;
 }
 
@@ -364,6 +390,8 @@ slikl_status slikl_key_weights(const slikl_problem *problem,
     const int u = 61 - bits < 40 ? 61 - bits : 40;
     a.one = (float)(int64_t(1) << u);
     a.sums = reinterpret_cast<unsigned long long *>(static_cast<char *>(workspace) + L.sums);
+    if (pr.layout_k == SLIKL_TND)
+        a.bad_k = reinterpret_cast<uint32_t *>(static_cast<char *>(workspace) + L.bad_k);
     a.status = tensors->status;
 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -381,8 +409,7 @@ slikl_status slikl_key_weights(const slikl_problem *problem,
         return cudaGetLastError() == cudaSuccess ? SLIKL_OK : SLIKL_ERR_CUDA;
     }
     const int64_t pairs = (T2 + 1) / 2;
-    weights_clear<<<(unsigned)std::min<int64_t>((pairs + 511) / 512, 2 * sms), 512, 0, s>>>(
-        reinterpret_cast<ulonglong2 *>(a.sums), pairs);
+    weights_clear<<<(unsigned)std::min<int64_t>((pairs + 511) / 512, 2 * sms), 512, 0, s>>>(a, pairs);
     if (cudaGetLastError() != cudaSuccess) return SLIKL_ERR_CUDA;
     if (T1 > 0) {
         const int64_t chunks = (range + kSplitKeys - 1) / kSplitKeys;

@@ -181,6 +181,28 @@ def test_key_weights_flags(lk):
         assert st & bit
 
 
+@pytest.mark.parametrize("rows,K", [(13, 50), (1000, 300)])      # both sides of 65536 slots a batch
+def test_key_weights_unusable_key_ranges(rows, K):
+    """Key ranges that overlap, leave rows out or lead outside are all emptied, as for the gradient: every
+    row of the result is written, as decay * scores, in place too."""
+    lk = 700
+    assert (rows * K > 2 * 65536) == (rows == 1000)
+    idx, w = draw_rows(51, [rows - 3, 3], [lk, lk], K)
+    scores = torch.rand(2 * lk, generator=torch.Generator().manual_seed(52))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for ck in ([0, 2100, 1400], [-7, 700, 1400], [0, 700, 1399], [5, 700, 1400], [0, 900, 800], [1400, 700, 0]):
+        status.zero_()
+        out = torch.full((2 * lk,), float("nan"), device="cuda")
+        kw = dict(decay=0.5, layout_q="TND", layout_k="TND", cu_seqlens_q=dev(cu([rows - 3, 3])),
+                  cu_seqlens_k=torch.tensor(ck, dtype=torch.int32, device="cuda"), status=status)
+        sli.key_weights(dev(w)[:, None], dev(idx)[:, None], dev(scores), out=out, **kw)
+        assert int(status) & sli.SLIKL_DEV_BAD_CU_SEQLENS_K
+        assert torch.equal(out.cpu(), 0.5 * scores), ck
+        own = dev(scores)
+        sli.key_weights(dev(w)[:, None], dev(idx)[:, None], own, out=own, **kw)
+        assert torch.equal(own.cpu(), 0.5 * scores), ck
+
+
 def test_key_weights_beyond_one_pass_of_p():
     """A hot key that every row names with its whole weight: the sum is exact."""
     T, S2 = 5000, 40
