@@ -190,13 +190,14 @@ __device__ __forceinline__ void form_turner(const Args &a, const Lane &t, const 
 #pragma unroll
     for (int i = 0; i < 4; ++i) g.c[i] = pair(1.f, 1.f), g.s[i] = pair(0.f, 0.f);
     if (t.turns) load_angles(a, t, pos, g);
-    const Pair minus = pair(-1.f, -1.f);
+    const Pair minus = pair(-1.f, -1.f), none = pair(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         o.c[i] = gain[i] * g.c[i];
         o.c[i + 4] = gain[i + 4] * g.c[i];
-        o.s[i] = gain[i + 4] * g.s[i] * minus;
-        o.s[i + 4] = gain[i] * g.s[i];
+        // (where nothing turns the partner's gain stays out of it, infinite or NaN as it may be)
+        o.s[i] = t.turns ? gain[i + 4] * g.s[i] * minus : none;
+        o.s[i + 4] = t.turns ? gain[i] * g.s[i] : none;
     }
 }
 

@@ -342,6 +342,25 @@ def test_dims_behind_the_rotated_ones_do_not_meet(pairs, N):
         assert torch.equal(got[..., 64:][torch.isfinite(x[..., 64:])], x[..., 64:][torch.isfinite(x[..., 64:])])
 
 
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+@pytest.mark.parametrize("pairs", [False, True])
+@pytest.mark.parametrize("N", [1, 16])
+def test_gains_of_dims_behind_the_rotated_ones_do_not_meet(kind, pairs, N):
+    """An infinite or NaN gain of a dim that is not turned spoils that dim alone."""
+    s = make(24, 4000, N, 128, 64, FP, kind)
+    cs, gain = table(50, 64), s["gain"].clone()
+    pos = torch.arange(4000, dtype=torch.int32) % 50
+    spoilt = (65, 90, 127)
+    for d, v in zip(spoilt, (float("inf"), float("nan"), float("-inf"))):
+        gain[d] = v
+    y = sli.qk_norm_rope(dev(s["x"]), None, dev(cs), pos_q=dev(pos), layout_q="TND", norm_q=kind, gain_q=dev(gain),
+                         rot_layout="pairs" if pairs else "halves")["q"].cpu().double()
+    value, bound = ref.norm_rope(s["x"].double(), kind, s["gain"], None, cs, pos, 64, pairs, EPS, FP)
+    rest = [d for d in range(128) if d not in spoilt]
+    inside("q", y[..., rest], (value[..., rest], bound[..., rest]))
+    assert not torch.isfinite(y[..., list(spoilt)]).any()
+
+
 def test_in_place():
     s = make(15, 100, 16, 128, 64, BF, "rms")
     cs = table(100, 64)
