@@ -575,8 +575,8 @@ SLIKL_API slikl_status slikl_grad_projected(const slikl_problem *problem,
  *
  * Weights are summed as 64-bit integers in units of 2^-u, u = min(40, 61 - ceil(log2(T1 * topk))),
  * so the result has the same bits whatever the order; each weight is rounded to a multiple of
- * 2^-u once. A valid slot's weight lies in [0, 2].
- * ---------------------------------------------------------------------------------------
+ * 2^-u once. A valid slot's weight lies in [0, 2]. The product with decay, and its sum with the
+ * weights', are formed in fp64 and rounded once.
  */
 typedef struct {
     const int32_t *sparse_indices;  /* int32 [.., 1, topk] as in slikl_tensors                   */
@@ -596,7 +596,7 @@ typedef struct {
 SLIKL_API slikl_status slikl_key_weights_workspace_size(const slikl_problem *problem,
                                                         size_t *workspace_bytes);
 SLIKL_API slikl_status slikl_key_weights(const slikl_problem *problem,
-                                         const slikl_key_weights_tensors *tensors, float decay,
+                                         const slikl_key_weights_tensors *tensors, double decay,
                                          void *workspace, size_t workspace_bytes, void *stream,
                                          const slikl_options *options);
 

@@ -241,7 +241,7 @@ def load_library() -> ctypes.CDLL:
                                              ctypes.c_size_t, VP, P(slikl_options)]
         lib.slikl_key_weights_workspace_size.argtypes = [P(slikl_problem), P(ctypes.c_size_t)]
         lib.slikl_key_weights.argtypes = [P(slikl_problem), P(slikl_key_weights_tensors),
-                                          ctypes.c_float, VP, ctypes.c_size_t, VP,
+                                          ctypes.c_double, VP, ctypes.c_size_t, VP,
                                           P(slikl_options)]
         lib.slikl_evict.argtypes = [P(slikl_evict_problem), P(slikl_evict_tensors), VP]
         lib.slikl_status_string.argtypes = [ctypes.c_int32]

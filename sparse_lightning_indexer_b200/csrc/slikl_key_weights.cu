@@ -21,6 +21,8 @@
 // split form is bound by its instructions (issue slots 58 %, the integer pipe 56 % in use) and by the
 // latency of its loads between them; more loads on their way, by registers or through shared memory,
 // were no faster.
+#include <float.h>
+
 #include <algorithm>
 
 #include "slikl_common.cuh"
@@ -34,7 +36,7 @@ struct WeightArgs {
     const int32_t *idx, *cu_q, *cu_k, *used_q, *used_k;
     const float *weights, *scores;
     float *out;
-    float decay;
+    double decay;
     float one;                // 2^u: the units of a weight of 1
     unsigned long long *sums; // [T2], in units
     uint32_t *bad_k;          // weights_clear's finding that cu_seqlens_k is unusable; null: BSND keys
@@ -211,7 +213,7 @@ __device__ void check_batches(const WeightArgs &a) {
 __device__ __forceinline__ float finished(const WeightArgs &a, unsigned long long sum, int64_t key) {
     // both products and their sum in fp64: the history loses no more than its own fp32 rounding
     double s = (double)(long long)sum * (1.0 / (double)a.one);
-    if (a.scores) s += (double)a.decay * (double)a.scores[key];
+    if (a.scores) s += a.decay * (double)a.scores[key];
     return (float)s;
 }
 
@@ -339,7 +341,7 @@ slikl_status slikl_key_weights_workspace_size(const slikl_problem *problem,
 }
 
 slikl_status slikl_key_weights(const slikl_problem *problem,
-                               const slikl_key_weights_tensors *tensors, float decay,
+                               const slikl_key_weights_tensors *tensors, double decay,
                                void *workspace, size_t workspace_bytes, void *stream,
                                const slikl_options *options) {
     if (!problem || !tensors) return SLIKL_ERR_PARAM_NULLPTR;
@@ -352,7 +354,7 @@ slikl_status slikl_key_weights(const slikl_problem *problem,
     if (st != SLIKL_OK) return st;
     const int64_t T1 = pr.layout_q == SLIKL_BSND ? pr.B * pr.S1 : pr.T1;
     const int64_t T2 = pr.layout_k == SLIKL_BSND ? pr.B * pr.S2 : pr.T2;
-    if (!(decay >= 0.f) || decay > 3.4e38f) return SLIKL_ERR_PARAM_INVALID;
+    if (!(decay >= 0.0) || decay > DBL_MAX) return SLIKL_ERR_PARAM_INVALID;
     if ((T1 > 0 && !tensors->weights) || (T2 > 0 && !tensors->out) || !workspace)
         return SLIKL_ERR_PARAM_NULLPTR;
     if (misaligned(tensors->weights, 4) || misaligned(tensors->scores, 4) ||
@@ -382,7 +384,7 @@ slikl_status slikl_key_weights(const slikl_problem *problem,
     a.used_q = options ? options->seq_used_q : nullptr;
     a.used_k = options ? options->seq_used_k : nullptr;
     a.weights = tensors->weights;
-    a.scores = decay == 0.f ? nullptr : tensors->scores;
+    a.scores = decay == 0.0 ? nullptr : tensors->scores;
     a.out = tensors->out;
     a.decay = decay;
     int bits = 0;                    // ceil(log2(slots)): the sum stays below 2^(1 + bits + u) <= 2^62

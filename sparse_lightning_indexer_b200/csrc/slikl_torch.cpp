@@ -396,7 +396,7 @@ py::tuple key_weights(Tensor weights, Tensor idx, Tensor scores, double decay, i
     Tensor ws;
     if (rc == SLIKL_OK) {
         ws = workspace_of(workspace, bytes, dev);
-        rc = slikl_key_weights(&pr, &tn, (float)decay, ws.data_ptr(), bytes_of(ws), stream_of(dev), &opt);
+        rc = slikl_key_weights(&pr, &tn, decay, ws.data_ptr(), bytes_of(ws), stream_of(dev), &opt);
     }
     return py::make_tuple(rc, result, ws);
 }

@@ -203,6 +203,16 @@ def test_key_weights_unusable_key_ranges(rows, K):
         assert torch.equal(own.cpu(), 0.5 * scores), ck
 
 
+@pytest.mark.parametrize("rows,K", [(4, 33), (700, 300)])        # both sides of 65536 slots
+@pytest.mark.parametrize("decay", [0.99, 1 / 3, 1e-45])
+def test_key_weights_decay_in_64_bits(rows, K, decay):
+    """What no slot names is the product with the decay that the caller gave, rounded once."""
+    scores = torch.rand(1, 5000, generator=torch.Generator().manual_seed(53)) * 10
+    idx = torch.full((1, rows, 1, K), -1, dtype=torch.int32, device="cuda")
+    got = sli.key_weights(torch.zeros(1, rows, 1, K, device="cuda"), idx, dev(scores), decay=decay)["scores"].cpu()
+    assert torch.equal(got, (scores.double() * decay).float())
+
+
 def test_key_weights_beyond_one_pass_of_p():
     """A hot key that every row names with its whole weight: the sum is exact."""
     T, S2 = 5000, 40
