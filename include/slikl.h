@@ -448,7 +448,8 @@ SLIKL_API slikl_status slikl_grad_recompute_p(const slikl_problem *problem,
  *
  * 8-bit checkpoints. A checkpoint of x is, for each head of each row, scale = max|x| / 448 (fp32;
  * 0 for a zero row, at least the smallest normal fp32 number otherwise) and the D values x / scale
- * rounded to e4m3. The forward call can write one beside y in the same pass, both calls can read
+ * rounded to e4m3. (The quotient is formed in fp32 as x times 1 / scale: a value that comes within
+ * 2^-21 of itself of the middle between two codes may go to either.) The forward call can write one beside y in the same pass, both calls can read
  * one in place of x, and the gradient is then the one at scale * value. A NaN stays
  * one; an infinity makes its row's scale infinite, and the whole row reads back as NaN.
  *
@@ -577,6 +578,7 @@ SLIKL_API slikl_status slikl_grad_projected(const slikl_problem *problem,
  * so the result has the same bits whatever the order; each weight is rounded to a multiple of
  * 2^-u once. A valid slot's weight lies in [0, 2]. The product with decay, and its sum with the
  * weights', are formed in fp64 and rounded once.
+ * ---------------------------------------------------------------------------------------
  */
 typedef struct {
     const int32_t *sparse_indices;  /* int32 [.., 1, topk] as in slikl_tensors                   */

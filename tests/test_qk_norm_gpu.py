@@ -186,6 +186,32 @@ def test_checkpoint_values(dtype, D):
     assert ((b - want).abs() <= want.abs() * (2.0 ** -24 + ref.HALF[dtype]) + tiny)[ok].all()
 
 
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_checkpoint_scale_and_codes_by_the_definition(dtype):
+    """The scale is max|x| / 448 rounded to fp32, bit by bit, and every code the one that x / scale rounds to
+    in whichever way the quotient's own error may lead: a reciprocal to 2 units (2^-22 of itself) and a
+    product's rounding (2^-24), less than 2^-21 together."""
+    g = torch.Generator().manual_seed(4)
+    x = (torch.randn(400, 16, 128, generator=g) * torch.exp(2 * torch.randn(400, 16, 1, generator=g))).to(dtype)
+    c = sli.checkpoint_pack(x.cuda())
+    scale, codes = c.scale.cpu(), c.values.cpu().float()
+    assert torch.equal(scale, x.float().abs().amax(-1) / 448)
+    quotient = x.double() / scale.double()[..., None]
+    either = [(quotient * (1 + f * 2.0 ** -21)).float().clamp(-448, 448).to(torch.float8_e4m3fn).float() for f in (-1, 1)]
+    assert ((codes == either[0]) | (codes == either[1])).all()
+    # that leaves most codes no choice: 448 x / max is a middle between codes only where 7 X = O M 2^l, X and M
+    # the significands and O one of the eight odd numbers from 17 to 31, so for at most 8 of the 128 (bf16)
+    # or 1024 X to a given M, and no significand is more than twice as likely as the average one
+    assert ((either[0] == either[1]).double().mean()) > 7 / 8
+    # every positive finite maximum
+    bits = torch.arange(1, 0x7c00 if dtype == FP else 0x7f80, dtype=torch.int16)
+    x = torch.zeros(len(bits), 1, 64, dtype=dtype)
+    x[:, 0, 17] = bits.view(dtype)
+    c = sli.checkpoint_pack(x.cuda())
+    want = (x[:, :, 17].float() / 448).clamp_min(2.0 ** -126)
+    assert torch.equal(c.scale.cpu(), want)
+
+
 def test_default_positions_and_batches():
     B, S, N, D, R = 3, 21, 4, 64, 32
     s = make(5, B * S, N, D, R, BF, "rms")
