@@ -1,5 +1,6 @@
-"""Builds the CUDA library libslikl.so in-tree with nvcc for sm_100a, and beside it _slikl_torch.so, the
-C++ marshalling of torch tensors for the calls whose latency counts (g++, no device code).
+"""Builds the CUDA library libslikl.so in-tree with nvcc for sm_100a, and beside it, where torch is installed,
+_slikl_torch.so, the C++ marshalling of torch tensors for the calls whose latency counts (g++, no device
+code). The library alone needs neither torch nor Python's headers.
 
 Usage: python -m sparse_lightning_indexer_b200.build [--force]
 """
@@ -7,9 +8,12 @@ Usage: python -m sparse_lightning_indexer_b200.build [--force]
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
+import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -43,7 +47,8 @@ def _stale(target: str, deps) -> bool:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile every csrc/*.cu into one shared library; returns its path."""
+    """Compile every csrc/*.cu into one shared library, and the torch binding where what it needs is
+    there; returns the library's path."""
     os.makedirs(OBJDIR, exist_ok=True)
     sources = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     headers = sorted(glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h")))
@@ -68,8 +73,29 @@ def build(force: bool = False, verbose: bool = False) -> str:
                *objs, "-lcuda"]
         subprocess.check_call(cmd)
         os.replace(tmp, LIB)
-    build_torch(force)
+    missing = _binding_lacks()
+    if missing:
+        sys.stderr.write(f"_slikl_torch.so is not built: no {missing}\n")
+    else:
+        build_torch(force)
     return LIB
+
+
+def _torch_root():
+    spec = importlib.util.find_spec("torch")
+    return os.path.dirname(spec.origin) if spec and spec.origin else None
+
+
+def _binding_lacks():
+    """What the torch binding needs and is not installed, or None."""
+    root = _torch_root()
+    if not root:
+        return "torch"
+    for path in (os.path.join(root, "lib", "libc10_cuda.so"), os.path.join(root, "include", "ATen", "ATen.h"),
+                 os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        if not os.path.exists(path):
+            return path
+    return None if shutil.which("g++") else "g++"
 
 
 def build_torch(force: bool = False) -> str:
@@ -78,8 +104,6 @@ def build_torch(force: bool = False) -> str:
     headers = glob.glob(os.path.join(INCLUDE, "*.h"))
     if not force and not _stale(TORCH_LIB, [src, os.path.abspath(__file__)] + headers):
         return TORCH_LIB
-    import sysconfig
-
     import torch
     troot = os.path.dirname(torch.__file__)
     includes = [os.path.join(troot, "include"), os.path.join(troot, "include", "torch", "csrc", "api", "include"),

@@ -6,6 +6,7 @@ import ctypes
 import os
 import shutil
 import subprocess
+import sys
 
 import pytest
 import torch
@@ -364,6 +365,20 @@ def test_binding_refuses_before_any_launch():
     ok = torch.zeros(4, 200)[:, 8:136].unflatten(1, (2, 64))
     assert sli._load_binding().row_stride(ok, "x") == 200 and sli._load_binding().row_stride(x, "x") == 128
     assert sli._load_binding().row_stride(torch.zeros(1, 1, 2, 64).expand(1, 1, 2, 64), "x") == 128
+
+
+def test_the_library_builds_without_torch(lib, tmp_path):
+    """A C user needs no torch: without it the build makes the library, says so, and succeeds."""
+    code = ("import importlib.util, sys\n"
+            f"spec = importlib.util.spec_from_file_location('b', {slibuild.__file__!r})\n"
+            "b = importlib.util.module_from_spec(spec)\n"
+            "spec.loader.exec_module(b)\n"
+            f"b.TORCH_LIB = {str(tmp_path / '_slikl_torch.so')!r}\n"
+            "assert importlib.util.find_spec('torch') is None\n"
+            "print(b.build())\n")
+    r = subprocess.run([sys.executable, "-I", "-S", "-c", code], capture_output=True, text=True, cwd=tmp_path)
+    assert r.returncode == 0, r.stderr
+    assert r.stdout.strip() == slibuild.LIB and "torch" in r.stderr and not os.listdir(tmp_path)
 
 
 @pytest.mark.skipif(shutil.which("gcc") is None, reason="needs gcc")
