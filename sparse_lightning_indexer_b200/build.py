@@ -8,6 +8,7 @@ Usage: python -m sparse_lightning_indexer_b200.build [--force]
 from __future__ import annotations
 
 import glob
+import importlib.metadata
 import importlib.util
 import os
 import shutil
@@ -99,10 +100,17 @@ def _binding_lacks():
 
 
 def build_torch(force: bool = False) -> str:
-    """Compile csrc/slikl_torch.cpp against torch's headers and libslikl.so; returns its path."""
+    """Compile csrc/slikl_torch.cpp against torch's headers and libslikl.so; returns its path. A module
+    built for another torch or Python than the installed ones is built anew."""
     src = os.path.join(CSRC, "slikl_torch.cpp")
     headers = glob.glob(os.path.join(INCLUDE, "*.h"))
-    if not force and not _stale(TORCH_LIB, [src, os.path.abspath(__file__)] + headers):
+    note = os.path.join(OBJDIR, os.path.basename(TORCH_LIB) + ".built_for.txt")
+    wanted = f"torch {importlib.metadata.version('torch')}, {sys.implementation.cache_tag}"
+    built_for = ""
+    if os.path.exists(note):
+        with open(note) as f:
+            built_for = f.read()
+    if not force and built_for == wanted and not _stale(TORCH_LIB, [src, os.path.abspath(__file__)] + headers):
         return TORCH_LIB
     import torch
     troot = os.path.dirname(torch.__file__)
@@ -123,6 +131,8 @@ def build_torch(force: bool = False) -> str:
         sys.stderr.write(res.stdout + res.stderr)
         raise RuntimeError(f"g++ failed on {src}")
     os.replace(tmp, TORCH_LIB)
+    with open(note, "w") as f:
+        f.write(wanted)
     return TORCH_LIB
 
 

@@ -3,6 +3,7 @@ checks, before a CUDA call (so they run without a GPU, with pointers that nothin
 binding's refusals, and the struct layouts against a C99 caller."""
 
 import ctypes
+import importlib.metadata
 import os
 import shutil
 import subprocess
@@ -379,6 +380,28 @@ def test_the_library_builds_without_torch(lib, tmp_path):
     r = subprocess.run([sys.executable, "-I", "-S", "-c", code], capture_output=True, text=True, cwd=tmp_path)
     assert r.returncode == 0, r.stderr
     assert r.stdout.strip() == slibuild.LIB and "torch" in r.stderr and not os.listdir(tmp_path)
+
+
+def test_the_binding_is_built_anew_for_another_torch(lib, tmp_path, monkeypatch):
+    """File times do not tell that torch or Python changed; what the module was built for does."""
+    built = []
+
+    def run(cmd, **kw):
+        built.append(cmd)
+        open(cmd[cmd.index("-o") + 1], "w").close()
+        return subprocess.CompletedProcess(cmd, 0, "", "")
+
+    monkeypatch.setattr(slibuild, "TORCH_LIB", str(tmp_path / "_slikl_torch.so"))
+    monkeypatch.setattr(slibuild, "OBJDIR", str(tmp_path))
+    monkeypatch.setattr(slibuild.subprocess, "run", run)
+    version = importlib.metadata.version
+    for torch_version, count in (("2.11.0", 1), ("2.11.0", 1), ("2.12.0", 2), ("2.12.0", 2), ("2.11.0", 3)):
+        monkeypatch.setattr(importlib.metadata, "version",
+                            lambda name, v=torch_version: v if name == "torch" else version(name))
+        assert slibuild.build_torch() == slibuild.TORCH_LIB
+        assert len(built) == count, torch_version
+    slibuild.build_torch(force=True)
+    assert len(built) == 4
 
 
 @pytest.mark.skipif(shutil.which("gcc") is None, reason="needs gcc")
