@@ -170,6 +170,7 @@ struct On {
     c10::cuda::OptionalCUDAStreamGuard stream;
     c10::cuda::OptionalCUDAGuard device;
     On(const at::Device &dev, const MaybeStream &s) {
+        if (s && s->device() != dev) refuse("stream is of ", s->device(), ", the tensors are on ", dev);
         if (s) stream.reset_stream(*s);
         device.set_device(dev);
     }

@@ -261,6 +261,23 @@ def test_key_weights_calls_in_flight_on_two_streams():
     assert all(torch.equal(g, v) for turn in got for g, v in zip(turn, want))
 
 
+def test_a_stream_of_another_device_is_refused():
+    """It could not order the call's work, which would have gone to the tensors' own device unordered."""
+    n = torch.cuda.device_count()
+    if n > 1:
+        other = torch.cuda.Stream(device=1)
+    else:
+        other = torch.Stream(stream_id=0, device_index=1, device_type=int(torch._C._autograd.DeviceType.CUDA))
+    s = torch.rand(1, 30, device="cuda:0")
+    w, i = torch.rand(1, 2, 1, 8, device="cuda:0"), torch.zeros(1, 2, 1, 8, dtype=torch.int32, device="cuda:0")
+    x = torch.zeros(4, 1, 64, dtype=torch.bfloat16, device="cuda:0")
+    for call in (lambda: sli.key_weights(w, i, s, stream=other), lambda: sli.evict(s, [], 4, stream=other),
+                 lambda: sli.qk_norm_rope(x, None, layout_q="TND", stream=other),
+                 lambda: sli.qk_norm_rope_grad(x, None, x, None, layout_q="TND", stream=other)):
+        with pytest.raises(ValueError, match="stream"):
+            call()
+
+
 def test_key_weights_without_queries_or_keys():
     e = torch.empty(0, 1, 8, device="cuda")
     s = torch.rand(30, device="cuda")
