@@ -278,6 +278,135 @@ def test_a_stream_of_another_device_is_refused():
             call()
 
 
+def slots_of(lq, K):
+    """Slots of the call, which the form for many of them takes above 65536 a batch on average."""
+    return sum(lq) * K, 65536 * len(lq)
+
+
+# more than 65536 slots a batch: ranges of one, two and three chunks of 55296 keys, uneven sequences with empty
+# ones on either side, more batches than multiprocessors can share, one long batch among short ones
+LARGE = [
+    ("BSND", [400], [60000], 300),
+    ("BSND", [300] * 2, [70000] * 2, 500),
+    ("BSND", [70] * 160, [300] * 160, 1000),
+    ("TND", [600], [131072], 300),
+    ("TND", [0, 700, 3, 500, 40], [40, 60000, 0, 9000, 55297], 400),
+    ("TND", [1, 2500, 1, 1], [55296, 110593, 77, 1], 128),
+    ("TND", [130 + 7 * (b % 5) for b in range(100)], [50 + 130 * (b % 9) for b in range(100)], 600),
+]
+
+
+@pytest.mark.parametrize("case", LARGE, ids=lambda c: f"{c[0]}-{len(c[1])}x{max(c[1])}-{max(c[2])}-{c[3]}")
+def test_key_weights_of_many_slots(case):
+    layout, lq, lk, K = case
+    slots, few = slots_of(lq, K)
+    assert slots > few
+    idx, w = draw_rows(61, lq, lk, K)
+    scores = torch.rand(sum(lk), generator=torch.Generator().manual_seed(62)) * 10
+    bsnd, B = layout == "BSND", len(lq)
+    lead = (B, lq[0]) if bsnd else (sum(lq),)
+    i, wd, s = dev(idx).reshape(*lead, 1, K), dev(w).reshape(*lead, 1, K), dev(scores).reshape((B, lk[0]) if bsnd else (-1,))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kw = dict(decay=0.7, layout_q=layout, layout_k=layout, cu_seqlens_q=None if bsnd else dev(cu(lq)),
+              cu_seqlens_k=None if bsnd else dev(cu(lk)), status=status)
+    r = sli.key_weights(wd, i, s, **kw)["scores"]
+    check_weights(r, idx, w, ranges(lq), ranges(lk), scores, 0.7)
+    # a promise about the longest range that is right, one that is not, and the result in place
+    for bound in () if bsnd else (max(lk), max(1, max(lk) // 3), 1):
+        assert torch.equal(sli.key_weights(wd, i, s, key_range_bound=bound, **kw)["scores"], r), bound
+    used_q = [n * (b % 4) // 3 for b, n in enumerate(lq)]
+    used_k = [n * (3 - b % 4) // 3 for b, n in enumerate(lk)]
+    i32 = dict(dtype=torch.int32, device="cuda")
+    ur = sli.key_weights(wd, i, s, seq_used_q=torch.tensor(used_q, **i32), seq_used_k=torch.tensor(used_k, **i32), **kw)["scores"]
+    check_weights(ur, idx, w, ranges(lq), ranges(lk), scores, 0.7, used_q, used_k)
+    sli.key_weights(wd, i, s, out=s, **kw)
+    assert torch.equal(s, r) and int(status) == 0
+
+
+@pytest.mark.parametrize("layout_q,layout_k", [("BSND", "TND"), ("TND", "BSND")])
+def test_key_weights_of_many_slots_in_mixed_layouts(layout_q, layout_k):
+    B, S1, S2, K = 3, 300, 60000, 300
+    assert B * S1 * K > 65536 * B
+    idx, w = draw_rows(63, [S1] * B, [S2] * B, K)
+    scores = torch.rand(B * S2, generator=torch.Generator().manual_seed(64))
+    lead = (B, S1) if layout_q == "BSND" else (B * S1,)
+    r = sli.key_weights(dev(w).reshape(*lead, 1, K), dev(idx).reshape(*lead, 1, K),
+                        dev(scores).reshape((B, S2) if layout_k == "BSND" else (B * S2,)), layout_q=layout_q,
+                        layout_k=layout_k, cu_seqlens_q=dev(cu([S1] * B)), cu_seqlens_k=dev(cu([S2] * B)))["scores"]
+    check_weights(r, idx, w, ranges([S1] * B), ranges([S2] * B), scores, 1.0)
+
+
+@pytest.mark.parametrize("lk", [900, 60000])
+def test_key_weights_flags_of_many_slots(lk):
+    """What breaks the contract in a large call is flagged, and touches nothing else."""
+    lq, K = [500, 4], 300
+    assert sum(lq) * K > 65536 * 2
+    idx, w = draw_rows(65, lq, [lk, lk], K, invalid=0.2)
+    scores = torch.zeros(2 * lk)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kw = dict(layout_q="TND", layout_k="TND", cu_seqlens_k=dev(cu([lk, lk])), status=status)
+
+    def run(idx, w, cq=cu(lq)):
+        status.zero_()
+        r = sli.key_weights(dev(w)[:, None], dev(idx)[:, None], dev(scores), cu_seqlens_q=dev(cq), **kw)
+        return r["scores"], int(status)
+
+    for bad in (lk, -2, 2 ** 31 - 1, -2 ** 31):
+        i2 = idx.clone()
+        i2[3, 7] = i2[501, 299] = bad
+        got, st = run(i2, w)
+        assert st == sli.SLIKL_DEV_INDEX_OUT_OF_RANGE
+        i2[3, 7] = i2[501, 299] = -1
+        check_weights(got, i2, w, ranges(lq), ranges([lk, lk]), scores, 1.0)
+    for bad, stands in ((-1.0, 0.0), (float("nan"), 0.0), (2.5, 2.0), (float("inf"), 2.0), (float("-inf"), 0.0)):
+        i2, w2 = idx.clone(), w.clone()
+        i2[3, 7], w2[3, 7], i2[501, 299], w2[501, 299] = 5, bad, lk - 1, bad
+        got, st = run(i2, w2)
+        assert st == sli.SLIKL_DEV_BAD_WEIGHT
+        w2[3, 7] = w2[501, 299] = stands
+        check_weights(got, i2, w2, ranges(lq), ranges([lk, lk]), scores, 1.0)
+    for cq in ([0, 700, 504], [0, 500, 503], [-5, 500, 504]):
+        got, st = run(idx, w, torch.tensor(cq, dtype=torch.int32))
+        assert st & sli.SLIKL_DEV_BAD_CU_SEQLENS_Q and torch.isfinite(got).all()
+    status.zero_()
+    sli.key_weights(dev(w)[:, None], dev(idx)[:, None], dev(scores), cu_seqlens_q=dev(cu(lq)),
+                    seq_used_q=torch.tensor([501, 4], dtype=torch.int32, device="cuda"), **kw)
+    assert int(status) == sli.SLIKL_DEV_BAD_SEQ_USED
+
+
+@pytest.mark.parametrize("rows,K", [(4, 8), (700, 300)])         # both sides of 65536 slots
+def test_key_weights_smallest_unit(rows, K):
+    """Units of 2^-40 up to 2^21 slots: a weight of one unit counts, half a unit (a tie, to even) does not,
+    and what lies above the half counts as one."""
+    w = torch.full((1, rows, 1, K), float("nan"))
+    idx = torch.full((1, rows, 1, K), -1, dtype=torch.int32)
+    for k, x in enumerate((2.0 ** -40, 2.0 ** -41, 2.0 ** -41 * (1 + 2.0 ** -23), 2.0 ** -42, 1.5 * 2.0 ** -40, 2.0)):
+        w[0, rows - 1, 0, k], idx[0, rows - 1, 0, k] = x, k
+    got = sli.key_weights(dev(w), dev(idx), torch.zeros(1, 10, device="cuda"))["scores"].cpu()[0].tolist()
+    unit = 2.0 ** -40
+    assert got == [unit, 0.0, unit, 0.0, 2 * unit, 2.0, 0.0, 0.0, 0.0, 0.0]
+
+
+def test_key_weights_two_graphs_share_a_workspace():
+    """Calls that keep their sums in the workspace, captured on one workspace and replayed in turn."""
+    idx, w = draw_rows(66, [700], [9000], 300)
+    i, s = dev(idx).view(1, 700, 1, 300), torch.rand(1, 9000, device="cuda")
+    ws, graphs = torch.empty(1 << 20, dtype=torch.uint8, device="cuda"), []
+    for scale in (1.0, 0.5):
+        wd = dev(w).view(1, 700, 1, 300) * scale
+        sli.key_weights(wd, i, s)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = sli.key_weights(wd, i, s, workspace=ws)["scores"]
+        graphs.append((g, out, wd))
+    for j in (0, 1, 1, 0, 1):
+        graphs[j][0].replay()
+    torch.cuda.synchronize()
+    for _, out, wd in graphs:
+        assert torch.equal(out, sli.key_weights(wd, i, s)["scores"])
+
+
 def test_key_weights_without_queries_or_keys():
     e = torch.empty(0, 1, 8, device="cuda")
     s = torch.rand(30, device="cuda")
@@ -358,6 +487,27 @@ def test_evict(case, kind):
         assert torch.equal(got[:m].view(torch.int32), scores[rows].view(torch.int32)) and (got[m:] == 0).all()
         for c, o in zip(caches, r["caches"]):
             assert torch.equal(o[b, :m].cpu(), c[rows]) and (o[b, m:] == 3).all()
+
+
+@pytest.mark.parametrize("bound", [20, 8192, 9001, 40000])
+@pytest.mark.parametrize("kind", ["normal", "same", "strange"])
+def test_evict_with_a_promise_about_the_longest_sequence(bound, kind):
+    """key_range_bound only chooses how many multiprocessors share a sequence; one that the lengths break
+    costs time, not rows."""
+    lens, budget, sinks, recent = [3000, 40000, 0, 20, 8192, 700, 9001], 600, 3, 50
+    scores = make_scores(14, sum(lens), kind)
+    c = torch.arange(4 * sum(lens), dtype=torch.int32).reshape(-1, 4)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    r = sli.evict(dev(scores), [dev(c)], budget, sinks=sinks, recent=recent, layout_k="TND", cu_seqlens_k=dev(cu(lens)),
+                  key_range_bound=bound, status=status)
+    assert int(status) == 0
+    for b, (at, n) in enumerate(ranges(lens)):
+        keep = ref.evict(scores[at: at + n], n, budget, sinks, recent)
+        m = len(keep)
+        assert int(r["lengths"][b]) == m and r["kept"][b].tolist() == keep + [-1] * (budget - m)
+        rows = at + torch.tensor(keep, dtype=torch.long)
+        assert torch.equal(r["scores"][b, :m].cpu().view(torch.int32), scores[rows].view(torch.int32))
+        assert torch.equal(r["caches"][0][b, :m].cpu(), c[rows]) and (r["caches"][0][b, m:] == 0).all()
 
 
 def test_evict_without_caches_and_default_outputs():

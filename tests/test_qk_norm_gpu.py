@@ -146,6 +146,60 @@ def test_sides_of_very_different_sizes(T1, N1, T2, source):
                 inside(f"{what}_{n}", both[f"{what}_{n}"], want[what])
 
 
+@pytest.mark.parametrize("D,T", [(128, 1800), (64, 3600)])
+@pytest.mark.parametrize("pairs", [False, True])
+@pytest.mark.parametrize("kind", ["none", "rms", "layer"])
+@pytest.mark.parametrize("source", ["x", "x8", "slices"])
+def test_two_rows_a_step(D, T, pairs, kind, source):
+    """Calls large enough for two rows of a token a step in both directions (16 heads; 28416 rows of 128 values
+    forward, 56832 of 64, half of that backward), from dense rows, checkpoints and slices of one
+    projection; padding rows with NaN among them; beside them keys of one head."""
+    N, R, dtype = 16, 48, FP if pairs else BF
+    assert T * N >= 2 * (512 // D) * 4 * 148 * 6
+    q, k = make(41, T, N, D, R, dtype, kind), make(42, T, 1, D, R, dtype, "rms")
+    g = torch.Generator().manual_seed(43)
+    cs, pos = table(700, R), torch.randint(0, 700, (T,), generator=g, dtype=torch.int32)
+    pos[[0, 17, T // 2, T - 1]] = -1
+    xq, xk, dq, dk = dev(q["x"]), dev(k["x"]), dev(q["dy"]), dev(k["dy"])
+    out = None
+    at = {"q": q["x"].double(), "k": k["x"].double()}
+    if source == "x8":
+        xq, xk = sli.checkpoint_pack(xq), sli.checkpoint_pack(xk)
+        at = {"q": dequant(xq), "k": dequant(xk)}
+        xq.values.view(torch.uint8)[dev(pos < 0)] = 0x7f                # NaN
+    else:
+        xq[dev(pos < 0)] = float("nan")
+    dq[dev(pos < 0)] = float("inf")
+    if source == "slices":
+        W = (N + 1) * D + 24
+        proj = torch.full((T, W), 5.0, dtype=dtype, device="cuda")
+        grads = torch.full((T, W), 7.0, dtype=dtype, device="cuda")
+
+        def cut(p):
+            return p[:, 8: 8 + N * D].unflatten(1, (N, D)), p[:, 16 + N * D: 16 + (N + 1) * D].unflatten(1, (1, D))
+
+        for to, v in zip(cut(proj), (xq, xk)):
+            to.copy_(v)
+        xq, xk = cut(proj)
+        out = dict(zip(("dx_q", "dx_k"), cut(grads)))
+    kw = dict(pos_q=dev(pos), pos_k=dev(pos), gain_q=dev(q["gain"]), gain_k=dev(k["gain"]), norm_q=kind,
+              layout_q="TND", layout_k="TND", rot_layout="pairs" if pairs else "halves", eps=EPS)
+    f = sli.qk_norm_rope(xq, xk, dev(cs), bias_q=dev(q["bias"]), checkpoint=source != "x8", **kw)
+    b = sli.qk_norm_rope_grad(dq, dk, xq, xk, dev(cs), out=out, **kw)
+    for n, s in (("q", q), ("k", k)):
+        inside(n, f[n], ref.norm_rope(at[n], s["kind"], s["gain"], s["bias"], cs, pos, R, pairs, EPS, dtype))
+        want = ref.norm_rope_grad(s["dy"].double(), at[n], s["kind"], s["gain"], cs, pos, R, pairs, EPS, dtype)
+        for what in ("dx", "dgain", "dbias"):
+            assert (b[f"{what}_{n}"] is None) == (want[what] is None)
+            if want[what] is not None:
+                inside(f"{what}_{n}", b[f"{what}_{n}"], want[what])
+        if source != "x8":
+            check_checkpoint(f["checkpoint_" + n], s["x"], pos)
+    if source == "slices":
+        for sl in (slice(0, 8), slice(8 + N * D, 16 + N * D), slice(16 + (N + 1) * D, W)):
+            assert (grads[:, sl] == 7).all()
+
+
 def check_checkpoint(c, x, pos=None):
     live = (pos >= 0)[:, None] if pos is not None else torch.ones(x.shape[:-1], dtype=torch.bool)
     x = torch.where(live[..., None], x.double(), 0.0)
