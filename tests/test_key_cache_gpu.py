@@ -598,6 +598,40 @@ def test_weights_then_eviction_then_the_gradient_on_the_smaller_cache():
         assert ((x - y).abs() <= 2 * 2.0 ** -8 * y.abs() + 2 * S1 * 16 * 2.0 ** -24 * terms).all()
 
 
+def test_structs_and_addresses_instead_of_tensors():
+    """The functions that take the C structs, for memory that is not torch's, do what those for tensors do."""
+    S1, S2, K, budget, D = 60, 3000, 128, 500, 64
+    idx, w = draw_rows(71, [S1], [S2], K)
+    i, w, s = dev(idx).reshape(1, S1, 1, K), dev(w).reshape(1, S1, 1, K), torch.rand(1, S2, device="cuda")
+    c = torch.randn(1, S2, D, device="cuda")
+    want = sli.key_weights(w, i, s, decay=0.9)["scores"]
+    cut = sli.evict(want, [c], budget, sinks=4, recent=8)
+    st = torch.cuda.current_stream().cuda_stream
+    pr = sli.slikl_problem(layout_q=sli.SLIKL_BSND, layout_k=sli.SLIKL_BSND, B=1, S1=S1, S2=S2, topk=K)
+    n = sli.slikl_key_weights_workspace_size(pr)
+    ws, out = torch.empty(n, dtype=torch.uint8, device="cuda"), torch.empty_like(s)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    tn = sli.slikl_key_weights_tensors(sparse_indices=i.data_ptr(), weights=w.data_ptr(), scores=s.data_ptr(),
+                                       out=out.data_ptr(), status=status.data_ptr())
+    sli.slikl_key_weights(pr, tn, 0.9, ws.data_ptr(), n, st)
+    assert torch.equal(out, want)
+    kept, lengths = torch.empty(1, budget, dtype=torch.int32, device="cuda"), torch.empty(1, dtype=torch.int32, device="cuda")
+    best, small = torch.empty(1, budget, device="cuda"), torch.empty(1, budget, D, device="cuda")
+    pr = sli.slikl_evict_problem(layout_k=sli.SLIKL_BSND, n_caches=1, B=1, S2=S2, budget=budget, sinks=4, recent=8)
+    tn = sli.slikl_evict_tensors(scores=out.data_ptr(), kept=kept.data_ptr(), lengths=lengths.data_ptr(),
+                                 scores_out=best.data_ptr(), status=status.data_ptr())
+    tn.caches[0] = (c.data_ptr(), small.data_ptr(), D * 4)
+    sli.slikl_evict(pr, tn, st)
+    assert torch.equal(kept, cut["kept"]) and torch.equal(lengths, cut["lengths"]) and torch.equal(best, cut["scores"])
+    assert torch.equal(small, cut["caches"][0]) and int(status) == 0
+    tn.caches[0] = (c.data_ptr(), kept.data_ptr() // 16 * 16, D * 4)
+    with pytest.raises(sli.SliklError):
+        sli.slikl_evict(pr, tn, st)
+    pr = sli.slikl_problem(layout_q=sli.SLIKL_BSND, layout_k=sli.SLIKL_BSND, B=1, S1=S1, S2=S2, topk=0)
+    with pytest.raises(sli.SliklError):
+        sli.slikl_key_weights(pr, sli.slikl_key_weights_tensors(), 1.0, ws.data_ptr(), n, st)
+
+
 def test_graph_and_other_stream():
     lq, lk, K = [64], [3000], 128
     idx, w = draw_rows(21, lq, lk, K)

@@ -605,6 +605,64 @@ def test_projected_gradient(layout, source, mode):
     assert sli.slikl_read_device_status(res["workspace"].data_ptr()) == sli.SLIKL_DEV_BAD_POSITION
 
 
+def test_structs_and_addresses_instead_of_tensors():
+    """The functions that take the C structs, for memory that is not torch's, do what those for tensors do."""
+    wl = si.small(seed=78, B=1, S1=40, S2=300, N1=16, D=128, K=96)
+    T1, T2, N1, D, R, dtype = wl.T1, wl.T2, wl.N1, wl.D, 64, wl.q.dtype
+    q, k = make(79, T1, N1, D, R, dtype, "rms"), make(80, T2, 1, D, R, dtype, "layer")
+    cs, pos = dev(table(400, R)), {n: torch.arange(T, dtype=torch.int32, device="cuda") for n, T in (("q", T1), ("k", T2))}
+    t = {n: {m: dev(s[m]) for m in ("x", "dy", "gain", "bias")} for n, s in (("q", q), ("k", k))}
+    xq, xk = t["q"]["x"].reshape(wl.q.shape), t["k"]["x"].reshape(wl.k.shape)
+    w, p, idx = dev(wl.w), dev(wl.p), dev(wl.idx)
+    kw = dict(pos_q=pos["q"], pos_k=pos["k"], gain_q=t["q"]["gain"], gain_k=t["k"]["gain"], norm_k="layer", eps=EPS)
+    fwd = sli.qk_norm_rope(xq, xk, cs, bias_k=t["k"]["bias"], checkpoint=True, **kw)
+    bwd = sli.qk_norm_rope_grad(t["q"]["dy"].view(wl.q.shape), t["k"]["dy"].view(wl.k.shape), xq, xk, cs, **kw)
+    both = sli.grad_projected(xq, xk, w, p, idx, cs, bias_k=t["k"]["bias"], deterministic=True, **kw)
+    qk = sli.slikl_qk_problem(dtype=sli.SLIKL_BF16 if dtype == BF else sli.SLIKL_FP16, rot_layout=sli.SLIKL_ROT_HALVES, D=D,
+                              rot_dim=R, table_rows=400, eps=EPS,
+                              q=sli.slikl_qk_side(T=T1, N=N1, norm=sli.SLIKL_NORM_RMS),
+                              k=sli.slikl_qk_side(T=T2, N=1, norm=sli.SLIKL_NORM_LAYER))
+    tn, held = sli.slikl_qk_tensors(cos_sin=cs.data_ptr()), {}
+    for n, side in (("q", tn.q), ("k", tn.k)):
+        x = t[n]["x"]
+        held[n] = dict(y=torch.empty_like(x), keep8=torch.empty(x.shape, dtype=torch.float8_e4m3fn, device="cuda"),
+                       keep8_scale=torch.empty(x.shape[:-1], device="cuda"), dx=torch.empty_like(x),
+                       dgain=torch.empty(D, device="cuda"))
+        if n == "k":
+            held[n]["dbias"] = torch.empty(D, device="cuda")
+            side.bias = t[n]["bias"].data_ptr()
+        for name, v in (*held[n].items(), ("x", x), ("dy", t[n]["dy"]), ("gain", t[n]["gain"]), ("positions", pos[n])):
+            setattr(side, name, v.data_ptr())
+    st = torch.cuda.current_stream().cuda_stream
+    sli.slikl_qk_norm_rope(qk, tn, st)
+    n_grad = sli.slikl_qk_norm_rope_grad_workspace_size(qk)
+    ws = torch.empty(n_grad, dtype=torch.uint8, device="cuda")
+    sli.slikl_qk_norm_rope_grad(qk, tn, ws.data_ptr(), n_grad, st)
+
+    def same(a, b):
+        return torch.equal(a.reshape(-1).view(torch.uint8), b.reshape(-1).view(torch.uint8))
+
+    for n in "qk":
+        assert same(held[n]["y"], fwd[n]) and same(held[n]["keep8"], fwd["checkpoint_" + n].values)
+        assert same(held[n]["keep8_scale"], fwd["checkpoint_" + n].scale) and same(held[n]["dx"], bwd["dx_" + n])
+        assert same(held[n]["dgain"], bwd["dgain_" + n])
+    assert same(held["k"]["dbias"], bwd["dbias_k"])
+    pr = sli.make_problem(xq, xk, idx, deterministic=True)
+    n_all = sli.slikl_grad_projected_workspace_size(pr, qk)
+    ws, dw, y = torch.empty(n_all, dtype=torch.uint8, device="cuda"), torch.empty_like(w), torch.empty_like(p)
+    main = sli.slikl_tensors(w=w.data_ptr(), attn_softmax_l1norm=p.data_ptr(), sparse_indices=idx.data_ptr(),
+                             dw=dw.data_ptr(), softmax_out=y.data_ptr())
+    sli.slikl_grad_projected(pr, qk, main, tn, ws.data_ptr(), n_all, st)
+    assert same(dw, both["dw"]) and same(y, both["softmax_out"]) and same(held["k"]["dbias"], both["dbias_k"])
+    for n in "qk":
+        assert same(held[n]["dx"], both["dx_" + n]) and same(held[n]["dgain"], both["dgain_" + n])
+    for call in (lambda: sli.slikl_qk_norm_rope(qk, sli.slikl_qk_tensors(), st),
+                 lambda: sli.slikl_qk_norm_rope_grad(qk, tn, ws.data_ptr(), n_grad - 1, st),
+                 lambda: sli.slikl_grad_projected(pr, qk, main, tn, ws.data_ptr(), n_all - 1, st)):
+        with pytest.raises(sli.SliklError):
+            call()
+
+
 @pytest.mark.parametrize("layout,positions", [("BSND", True), ("BSND", False), ("TND", True)])
 @pytest.mark.parametrize("source", ["x", "x8"])
 def test_projected_gradient_of_a_padded_batch(layout, positions, source):
