@@ -203,6 +203,31 @@ def test_key_weights_unusable_key_ranges(rows, K):
         assert torch.equal(own.cpu(), 0.5 * scores), ck
 
 
+def test_key_weights_of_many_short_sequences():
+    """More sequences than every block looks at, TND, with used lengths and empty ones; unusable ranges among
+    them empty all."""
+    B, K = 3000, 24
+    lq, lk = [b % 3 for b in range(B)], [(7 * b) % 31 for b in range(B)]
+    assert sum(lq) * K <= 65536 * B
+    idx, w = draw_rows(54, lq, lk, K)
+    scores = torch.rand(sum(lk), generator=torch.Generator().manual_seed(55))
+    used_k = [max(0, n - b % 4) for b, n in enumerate(lk)]
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kw = dict(decay=0.5, layout_q="TND", layout_k="TND", cu_seqlens_q=dev(cu(lq)), status=status)
+    for bound in (0, 31, 5):
+        got = sli.key_weights(dev(w)[:, None], dev(idx)[:, None], dev(scores), cu_seqlens_k=dev(cu(lk)), key_range_bound=bound,
+                              seq_used_k=torch.tensor(used_k, dtype=torch.int32, device="cuda"), **kw)["scores"]
+        check_weights(got, idx, w, ranges(lq), ranges(lk), scores, 0.5, None, used_k)
+        assert int(status) == 0
+    broken = cu(lk)
+    broken[1700] += 500
+    for bound in (0, 31, 5):
+        got = torch.full((sum(lk),), float("nan"), device="cuda")
+        sli.key_weights(dev(w)[:, None], dev(idx)[:, None], dev(scores), cu_seqlens_k=dev(broken), key_range_bound=bound,
+                        out=got, **kw)
+        assert int(status) & sli.SLIKL_DEV_BAD_CU_SEQLENS_K and torch.equal(got.cpu(), 0.5 * scores)
+
+
 @pytest.mark.parametrize("rows,K", [(4, 33), (700, 300)])        # both sides of 65536 slots
 @pytest.mark.parametrize("decay", [0.99, 1 / 3, 1e-45])
 def test_key_weights_decay_in_64_bits(rows, K, decay):
