@@ -438,12 +438,14 @@ SLIKL_API slikl_status slikl_grad_recompute_p(const slikl_problem *problem,
  *   no norm     z = x
  * then, for the first rot_dim dims, y = z turned by the row's angles, (a, b) ->
  * (a cos - b sin, b cos + a sin), where (a, b) are dims (i, i + rot_dim/2) (SLIKL_ROT_HALVES) or
- * (2i, 2i + 1) (SLIKL_ROT_PAIRS), i < rot_dim/2; the other dims are y = z. Sums are fp32, and y is
- * rounded once to the 16-bit type. (A head's row with an infinity, or with a bf16 x whose squares overflow
- * fp32, |x| above about 1e18, is outside the norms' range: its y and dx may be NaN in every dim.)
+ * (2i, 2i + 1) (SLIKL_ROT_PAIRS), i < rot_dim/2; the other dims are y = z. Sums are fp32, r is
+ * fp32's rsqrt (within 2 units in the last place), and y is rounded once to the 16-bit type. (A
+ * head's row with an infinity, or with a bf16 x whose squares overflow fp32, |x| above about 1e18, is
+ * outside the norms' range: its y and dx may be NaN in every dim.)
  *
  * The gradient, with dz = dy turned back and xhat = (x - m) r (m = 0 for RMS):
- *   dgain = sum dz xhat, dbias = sum dz   (over all heads of all rows; fp32, the same bits each call)
+ *   dgain = sum dz xhat, dbias = sum dz   (over all heads of all rows; fp32, the same bits each call;
+ *                                          one thread adds up about one head row in 7000)
  *   u = dz gain,  dx = r (u - [layer: mean(u)] - xhat mean(u xhat));  no norm: dx = dz.
  *
  * 8-bit checkpoints. A checkpoint of x is, for each head of each row, scale = max|x| / 448 (fp32;
@@ -576,7 +578,9 @@ SLIKL_API slikl_status slikl_grad_projected(const slikl_problem *problem,
  *
  * Weights are summed as 64-bit integers in units of 2^-u, u = min(40, 61 - ceil(log2(T1 * topk))),
  * so the result has the same bits whatever the order; each weight is rounded to a multiple of
- * 2^-u once. A valid slot's weight lies in [0, 2]. The product with decay, and its sum with the
+ * 2^-u once. The sum is off by up to 2^-(u+1) for each slot that names the key, whatever its size:
+ * sums below about 2^(23-u) have fewer than fp32's digits (u = 40 up to 2^21 slots, 37 at 2^24), and
+ * weights of 2^-(u+1) and less add nothing. A valid slot's weight lies in [0, 2]. The product with decay, and its sum with the
  * weights', are formed in fp64 and rounded once.
  * ---------------------------------------------------------------------------------------
  */

@@ -761,6 +761,8 @@ def qk_norm_rope(x_q, x_k, cos_sin=None, *, pos_q=None, pos_k=None, gain_q=None,
     int32 positions per row (-1: padding row, all zero); without them a BSND row stands at its place
     in its batch. `status` (int32 [1]) receives SLIKL_DEV_BAD_POSITION. `stream`: as the current one.
     Returns dict(q, k) and, with checkpoint=True, checkpoint_q / checkpoint_k; `out` may supply q, k.
+    Like grad() and the functions below, this records nothing for autograd: results are detached, whether
+    the inputs require a gradient or not.
     """
     out_q, out_k = (out.get("q"), out.get("k")) if out else (None, None)
     rc, q, k, *kept = _load_binding().qk_forward(
@@ -784,7 +786,8 @@ def qk_norm_rope_grad(dq, dk, x_q, x_k, cos_sin=None, *, pos_q=None, pos_k=None,
     """The gradient of qk_norm_rope at x (or its Checkpoint): dq, dk as grad() returns them back to
     the projections. Returns dict(dx_q, dx_k, dgain_q, dgain_k, dbias_q, dbias_k, workspace); a
     side without a norm has no dgain, one without a layer norm no dbias. `out` may supply
-    dx_q / dx_k, whose rows may lie apart (slices of one projection's gradient)."""
+    dx_q / dx_k, whose rows may lie apart (slices of one projection's gradient). The dgain and dbias of
+    a call lie in one allocation, which lives as long as any of them."""
     out_q, out_k = (out.get("dx_q"), out.get("dx_k")) if out else (None, None)
     rc, dx_q, dx_k, dgain_q, dbias_q, dgain_k, dbias_k, ws = _load_binding().qk_gradient(
         dq, dk, *_sources(x_q, x_k), cos_sin, pos_q, pos_k, gain_q, gain_k,
@@ -892,7 +895,10 @@ def key_weights(weights, sparse_indices, scores, *, decay=1.0, layout_q="BSND", 
     """decay * scores plus, for every key row, the weights of the slots that name it
     (slikl_key_weights): fp32 `weights` and int32 `sparse_indices` [B,S1,1,topk] / [T1,1,topk] (p of
     grad(), softmax_out, or p of grad_recompute_p), fp32 `scores` [B,S2] / [T2]. `out` may be
-    `scores`. `status` (int32 [1]) receives the device flags. Returns dict(scores, workspace)."""
+    `scores`. A weight is at least 0 and at most 2: larger ones count as 2, negative ones and NaN as 0, which
+    SLIKL_DEV_BAD_WEIGHT in `status` (int32 [1], optional) tells, as its other flags tell of indices, lengths
+    and cu_seqlens that break the contract. TND: `key_range_bound`, the keys of the longest sequence, saves
+    time where there are several; a wrong one costs time. Returns dict(scores, workspace)."""
     rc, new, ws = _load_binding().key_weights(
         weights, sparse_indices, scores, decay, _LAYOUTS.get(layout_q, -1), _LAYOUTS.get(layout_k, -1),
         cu_seqlens_q, cu_seqlens_k, seq_used_q, seq_used_k, key_range_bound, out, workspace, status, stream)
@@ -908,8 +914,9 @@ def evict(scores, caches: Sequence[torch.Tensor], budget, *, sinks=0, recent=0, 
     tensors [B,S2,..] / [T2,..] of any type whose rows (a multiple of 16 bytes) go along.
     Returns dict(kept, lengths, scores, caches): local indices [B,budget] (-1 behind the last),
     rows kept [B] (the seq_used_k of the result), their scores, and the caches [B,budget,..].
-    `out` may supply any of the four; rows of its caches behind the last kept one are left as they
-    were (without it they are zero)."""
+    `out` may supply any of the four, none of which may share memory with an input or another output
+    (lengths may be seq_used_k); rows of its caches behind the last kept one are left as they were (without
+    it they are zero). Without `out`, kept and lengths lie in one allocation."""
     get = (out or {}).get
     rc, kept, lengths, new, outs = _load_binding().evict(
         scores, caches, budget, sinks, recent, _LAYOUTS.get(layout_k, -1), cu_seqlens_k, seq_used_k,

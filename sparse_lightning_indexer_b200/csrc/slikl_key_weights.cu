@@ -16,8 +16,9 @@
 //                   ranges are covered by several blocks that read the same slots, from L2 mostly)
 //                   and add them to 64-bit sums in the workspace once, which weights_clear has set to
 //                   zero; weights_finish makes the result. Each starts up while the one before it runs.
-// Measured on B200: 4 to 5 us for 32 rows of 2048 slots over 8192 keys each, 19 us for 8.4 M slots over 4096 keys
-// (3.5 TB/s of slots; floor 10.4), 68 us for 16.8 M over 131072 (floor 21; three blocks read each slot). The
+// Measured on B200 on the device (replays of a graph): 4 to 5 us for 32 rows of 2048 slots over 8192 keys
+// each, 19 us for 8.4 M slots over 4096 keys, a quarter of them empty (58.7 MB, which take 9.1 us at the copy
+// rate), 68 us for 16.8 M over 131072 (floor 21; three blocks read each slot). The
 // split form is bound by its instructions (issue slots 58 %, the integer pipe 56 % in use) and by the
 // latency of its loads between them; more loads on their way, by registers or through shared memory,
 // were no faster.
@@ -415,8 +416,12 @@ slikl_status slikl_key_weights(const slikl_problem *problem,
     // longest key range: known, promised, or all keys
     const int64_t range = std::min(pr.S2 > 0 ? pr.S2 : T2, T2);
     // A block of the direct form reads every slot of its batch, so that form is for few of them: up to
-    // 65536 a batch (on average, where lengths differ) its time stays below the other form's three
-    // launches.
+    // 65536 a batch on average. Measured on the device with equal batches, direct / split: 8192 slots of one
+    // batch of 4096 keys 5.2 / 7.3 us, 16384 7.2 / 8.1, 32768 10.3 / 8.2, 65536 17.5 / 8.2; of 32 batches of
+    // 8192 keys 7.2 / 9.3, 9.5 / 9.8, 14.4 / 11.6, 24.6 / 16.4: they meet near 20000 slots, above which the
+    // direct form saves the host two launches. Neither form looks at how uneven batches are, and the longest
+    // sets the time: 8192 rows beside 31 sequences of 128 (2048 slots a row) 1755 us where 32 equal ones take
+    // 173, a prompt of 3000 rows beside 127 single tokens 1700 us (direct).
     if (T1 * pr.topk <= 65536 * pr.B && pr.B <= 65535) {
         // chunks of 256 to 2048 keys, two blocks a multiprocessor where there are as many
         int64_t chunk = 256;

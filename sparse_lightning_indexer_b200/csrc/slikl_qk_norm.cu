@@ -19,9 +19,10 @@
 // the issue slots count (a row of 16 values a thread took 420 instructions in the gradient, which
 // kept it at half the copy rate; it is 224 now): arithmetic runs on pairs of fp32 values, addresses
 // are stepped along the warp's rows instead of computed, and two rows of a token share what is not
-// arithmetic. Measured on B200 in a run of calls (of the measured copy rate): 4096 rows of 64 heads of
-// 128 with their checkpoint 32 us (83 %), 34117 rows of 32 heads in fp16 110 us (82 %), the
-// gradient of 4096 rows 43 us (75 %), that of 32768 rows of 16 heads at their checkpoint 83 us (68 %).
+// arithmetic. Measured on B200 on the device, as replays of a graph (of the measured copy rate): 4096 rows of
+// 64 heads of 128 with their checkpoint 33 us (82 %), 34117 rows of 32 heads in fp16 110 to 115 us (78 to
+// 82 %, by the machine), the gradient of 4096 rows 42 us (75 %), that of 32768 rows of 16 heads at their
+// checkpoint 83 us (68 %).
 #include <cuda_fp8.h>
 #include <float.h>
 
@@ -1015,8 +1016,9 @@ int sm100_multiprocessors() {
 // side with rows gets one at least. A row of a token with few heads, for which angles come from the
 // table, takes 1 + few / N times as long as one of many heads (measured over shares on B200: with
 // few = 0.6 the varlen forward took 122 us, with 3 110; the gradient at the checkpoint 94 with 0.6,
-// 84 with 1.1 and 2, 88 with 3), and a layer norm 1.25 times as long as an RMS norm. A small call gets
-// a group of rows for each warp, so that it spreads over all multiprocessors.
+// 84 with 1.1 and 2, 88 with 3), and a layer norm 1.25 times as long as an RMS norm (with 1, 1.25 and 1.6
+// the gradient at the checkpoint took 84.9, 83.4 and 86.4 us, the forward with its checkpoint 33.1,
+// 32.9 and 33.6). A small call gets a group of rows for each warp, so that it spreads over all multiprocessors.
 void share_blocks(Args &a, int64_t D, int sms, int per_sm, double few) {
     const uint32_t most = (uint32_t)(std::min(sms, kMaxSms) * per_sm), warps = kThreads / 32;
     const uint32_t rpw = (uint32_t)(512 / D);
