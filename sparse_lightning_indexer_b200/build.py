@@ -105,7 +105,11 @@ def build_torch(force: bool = False) -> str:
     src = os.path.join(CSRC, "slikl_torch.cpp")
     headers = glob.glob(os.path.join(INCLUDE, "*.h"))
     note = os.path.join(OBJDIR, os.path.basename(TORCH_LIB) + ".built_for.txt")
-    wanted = f"torch {importlib.metadata.version('torch')}, {sys.implementation.cache_tag}"
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:       # a torch that no package manager put there
+        version = _torch_root()
+    wanted = f"torch {version}, {sys.implementation.cache_tag}"
     built_for = ""
     if os.path.exists(note):
         with open(note) as f:

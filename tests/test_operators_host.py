@@ -403,6 +403,14 @@ def test_the_binding_is_built_anew_for_another_torch(lib, tmp_path, monkeypatch)
     slibuild.build_torch(force=True)
     assert len(built) == 4
 
+    def unknown(name):
+        raise importlib.metadata.PackageNotFoundError(name)
+
+    monkeypatch.setattr(importlib.metadata, "version", unknown)
+    slibuild.build_torch()
+    slibuild.build_torch()
+    assert len(built) == 5
+
 
 @pytest.mark.skipif(shutil.which("gcc") is None, reason="needs gcc")
 def test_layouts_match_a_c_caller(lib, tmp_path):
